@@ -363,6 +363,151 @@ int proj_read_probe(const void *buf, size_t bytes, float *sink,
 int proj_ring_probe(const void *x, const void *w, int K, int rows, int piece, int depth,
                     int barrier, int what, int shared_w, int grid, float *sink, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Layer operators: what stands before, between and after the projections of
+ * a layer.  Every call below only launches kernels on `stream` (no
+ * allocation, memset, attribute change or synchronisation), so each may be
+ * recorded into a graph; operands are device pointers on the current device.
+ * Outputs must not overlap inputs or each other, where an operand of strided
+ * rows counts with the whole range from its first byte to its last; an
+ * overlap returns PROJ_EINVAL.
+ * ------------------------------------------------------------------------ */
+
+#define PROJ_MAX_ROW 32768       /* longest row of the norm and the codes  */
+#define PROJ_I8_MAX_K 131056     /* longest sum of 8-bit products (int32)  */
+#define PROJ_KERNEL_I8_PIPE 7    /* tactic kernel of the 8-bit projection  */
+#define PROJ_DELTA_HEAD 128      /* key and value size of a head           */
+#define PROJ_DELTA_MAX_HEADS 1024
+#define PROJ_DELTA_MAX_REQUESTS 4096
+#define PROJ_DELTA_MAX_TOKENS 1024
+#define PROJ_DELTA_MAX_ROWS (1 << 28)
+
+/*
+ * proj_rms_norm -- root-mean-square norm of rows, with the residual's
+ * addition before it and an output in BF16, in 8-bit codes, or both:
+ *     h = x + residual (h = x without one);  residual <- h, rounded
+ *     y = h * weight / sqrt(mean(h^2) + eps)
+ *     scale = max|y| / 127,  codes = round(y / scale), ties to even
+ * The norm takes the unrounded FP32 sum h, and the codes take the unrounded
+ * y.  The codes of a row of zeros are 0 with scale 0; a row with an infinity
+ * or a NaN gets codes 0 and scale NaN, so that products with it are NaN.
+ * The sum of squares is held in FP32: a row whose sum passes 3.4e38 comes
+ * out as zeros.
+ *   rows, D  : rows >= 0 (0 is a no-op); 8 <= D <= PROJ_MAX_ROW, D % 8 == 0
+ *   x        : BF16 [rows, D], row stride ldx (0 = D; ldx % 8 == 0)
+ *   residual : NULL, or [rows, D] BF16 (FP32 with residual_fp32 = 1), row
+ *              stride ldr (0 = D; ldr % 8 == 0), read and rewritten
+ *   weight   : BF16 [D]
+ *   y        : NULL, or BF16 [rows, D], contiguous
+ *   codes    : NULL, or int8 [rows, D], contiguous; scale: FP32 [rows], given
+ *              with codes.  One of y and codes at least.
+ * x, residual, weight and y are 16-byte aligned, codes 8, scale 4.
+ * Returns PROJ_OK, PROJ_EINVAL, PROJ_EALIGN or PROJ_EHIP.
+ */
+int proj_rms_norm(int rows, int D, const void *x, long ldx, void *residual, long ldr,
+                  int residual_fp32, const void *weight, float eps, void *y, void *codes,
+                  void *scale, void *stream);
+
+/*
+ * proj_quant_rows -- 8-bit codes of rows, without a norm: scale = max|x| /
+ * 127 and codes = round(x / scale) a row, with the same readings of zero and
+ * non-finite rows.  A weight [N, K] takes a scale per output channel this
+ * way, rows of activations one per token.
+ */
+int proj_quant_rows(int rows, int D, const void *x, long ldx, void *codes, void *scale,
+                    void *stream);
+
+/*
+ * proj_i8_plan / proj_i8_run -- the projection in 8-bit integers, with a
+ * scale per row of x (token) and per row of W (output channel):
+ *     y[b, n] = bf16( (sum_k x[b, k] * W[n, k]) * (x_scale[b] * w_scale[n]) )
+ * The integer sum is exact, so results do not depend on how K is split.
+ * Plans, bins, flags (PROJ_PLAN_HOST_ONLY only) and the workspace (one
+ * stream at a time) are those of proj_plan; K % 16 == 0 and K <=
+ * PROJ_I8_MAX_K besides.
+ *   x  : int8 [B, K] codes (-128..127), row stride ldx bytes (0 = K; ldx % 16
+ *        == 0), 16-byte aligned;  x_scale: FP32 [B]
+ *   W  : int8 [N, K], contiguous, 16-byte aligned;  w_scale: FP32 [N]
+ *   y  : BF16 [B, N], contiguous, 16-byte aligned
+ * Errors as proj_plan and proj_run.
+ */
+typedef struct proj_i8_plan_s proj_i8_plan_t;
+int proj_i8_plan(int N, int K, const int *batches, int n_batches, unsigned flags,
+                 proj_i8_plan_t **out);
+int proj_i8_run(const proj_i8_plan_t *plan, int B, const void *x, long ldx, const void *x_scale,
+                const void *W, const void *w_scale, void *y, void *stream);
+void proj_i8_free(proj_i8_plan_t *plan);
+/* As proj_plan_tactic, proj_plan_set_tactic and proj_plan_workspace_bytes;
+ * kernel is PROJ_KERNEL_I8_PIPE, kc counts K bytes a step. */
+int proj_i8_plan_tactic(const proj_i8_plan_t *plan, int B, proj_tactic_t *tactic, int *bin);
+int proj_i8_plan_set_tactic(proj_i8_plan_t *plan, int bin, const proj_tactic_t *tactic);
+size_t proj_i8_plan_workspace_bytes(const proj_i8_plan_t *plan);
+
+/*
+ * The gated delta rule.  A head's state S is a 128 x 128 matrix [key][value];
+ * a token with key k, query q, value v, decay a and strength beta does
+ *     S <- diag(a) S;  u = beta (v - S^T k);  S <- S + k u^T;  o = S^T q
+ * with a = exp(-exp(a_log[h]) * softplus(f + dt_bias)), a channel of the key
+ * each (or, with head_gate, one a head), beta = sigmoid(b), q and k divided
+ * by sqrt(|.|^2 + 1e-6) where l2norm is set, and q multiplied by scale.
+ * The operands of both forms (rows are tokens; strides in elements, 0 =
+ * contiguous; a row's heads are contiguous, so the columns of a packed
+ * projection output can be passed in place):
+ *   q, k    : BF16 [rows, qk_heads, 128], stride % 8 == 0
+ *   v, out  : BF16 [rows, heads, 128], stride % 8 == 0; value head h uses key
+ *             head h / (heads / qk_heads)
+ *   f       : BF16 [rows, heads, 128] (stride % 8 == 0), or [rows, heads]
+ *             with head_gate
+ *   b       : BF16 [rows, heads]
+ *   a_log   : FP32 [heads];  dt_bias: FP32 [heads, 128], or [heads]
+ *   state   : FP32 [n_slots, heads, 128, 128], contiguous, rewritten
+ * q, k, v, out, state, dt_bias and a per-channel f are 16-byte aligned.
+ */
+typedef struct proj_delta_io {
+    const void *q, *k, *v, *f, *b;
+    long ldq, ldk, ldv, ldf, ldb;
+    const void *a_log, *dt_bias;
+    void *state;
+    void *out;
+    long ldo;
+    float scale;
+    int l2norm;
+    int head_gate;
+} proj_delta_io_t;
+
+/*
+ * proj_delta_step -- the recurrent form, for decode and verify steps: request
+ * i has rows [i * tokens, (i + 1) * tokens) and continues the state slots[i].
+ *   requests : 0 .. PROJ_DELTA_MAX_REQUESTS;  tokens: 1 ..
+ *              PROJ_DELTA_MAX_TOKENS;  heads % qk_heads == 0
+ *   slots    : int32 [requests] on the device.  A slot outside 0 .. n_slots-1
+ *              (-1 by convention) is padding: its rows of out become zero and
+ *              no state is touched.  Requests that name one slot run in the
+ *              order of their rows.
+ */
+int proj_delta_step(const proj_delta_io_t *io, int heads, int qk_heads, int requests, int tokens,
+                    const void *slots, int n_slots, void *stream);
+
+/*
+ * proj_delta_plan / proj_delta_run -- sequences of many tokens (prompts, or
+ * pieces of them).  The plan is made once for a batch of sequences and
+ * serves every layer: sequence i has lens[i] rows (0 allowed), packed one
+ * after another, and continues the state slots[i].
+ *   lens, slots : host arrays of n (not retained); slots in 0 .. n_slots-1,
+ *                 no two alike; the lengths sum to at most
+ *                 PROJ_DELTA_MAX_ROWS
+ *   flags       : 0 or PROJ_PLAN_HOST_ONLY
+ * Rows of out past the last sequence are left as they were.  The plan owns
+ * its device workspace (one stream at a time, like proj_plan's), and making
+ * one waits for the device.  Errors as proj_plan and proj_run.
+ */
+typedef struct proj_delta_plan_s proj_delta_plan_t;
+int proj_delta_plan(int heads, int qk_heads, int n, const int *lens, const int *slots,
+                    int n_slots, unsigned flags, proj_delta_plan_t **out);
+int proj_delta_run(const proj_delta_plan_t *plan, const proj_delta_io_t *io, void *stream);
+long proj_delta_plan_rows(const proj_delta_plan_t *plan);
+void proj_delta_free(proj_delta_plan_t *plan);
+
 #ifdef __cplusplus
 }
 #endif

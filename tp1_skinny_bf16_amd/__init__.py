@@ -15,5 +15,9 @@ from ._binding import (EXPORTS, KERNEL_IDS, KERNEL_NAMES,  # noqa: F401
                        PROJ_OK, Plan, ProjError, Tactic, library, pack_rows, pack_rows_ptr,
                        prefetch, read_probe, ring_probe, run_noalloc, run_noalloc_ptr,
                        strerror)
+from ._binding import KERNEL_I8_PIPE  # noqa: F401
+from .delta import DeltaPlan, delta_step  # noqa: F401
 from .front import MoeFront  # noqa: F401
 from .layers import LayerStack  # noqa: F401
+from .norm import quant_rows, rms_norm, rms_norm_i8  # noqa: F401
+from .proj_i8 import PlanI8  # noqa: F401

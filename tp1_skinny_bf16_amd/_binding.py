@@ -27,6 +27,7 @@ KERNEL_STREAM = 1
 KERNEL_STREAM_DOT2 = 3
 KERNEL_MFMA_XS = 5
 KERNEL_MFMA_PIPE = 6
+KERNEL_I8_PIPE = 7            # the 8-bit projection's (PlanI8 only)
 KERNEL_NAMES = {KERNEL_STREAM: "stream", KERNEL_STREAM_DOT2: "stream_dot2",
                 KERNEL_MFMA_XS: "mfma_xs", KERNEL_MFMA_PIPE: "mfma_pipe"}
 KERNEL_IDS = {v: k for k, v in KERNEL_NAMES.items()}
@@ -36,13 +37,19 @@ PLAN_SPLIT_FUSED = 0x2
 MAX_BATCH = 256
 MAX_BATCHES = 64
 MAX_PACK = 64
+MAX_ROW = 32768              # longest row of the norm and the codes
+MAX_I8_K = 131056            # longest sum of 8-bit products
 
 # every symbol include/tp1_proj.h declares
 EXPORTS = ("proj_plan", "proj_run", "proj_free", "proj_strerror",
            "proj_plan_tactic", "proj_plan_set_tactic",
            "proj_plan_workspace_bytes", "proj_read_probe", "proj_run_layers",
            "proj_plan_kernel_name", "proj_run_noalloc", "proj_prefetch",
-           "proj_run_layers_overlap", "proj_pack_rows", "proj_ring_probe")
+           "proj_run_layers_overlap", "proj_pack_rows", "proj_ring_probe",
+           "proj_rms_norm", "proj_quant_rows", "proj_i8_plan", "proj_i8_run", "proj_i8_free",
+           "proj_i8_plan_tactic", "proj_i8_plan_set_tactic", "proj_i8_plan_workspace_bytes",
+           "proj_delta_step", "proj_delta_plan", "proj_delta_run", "proj_delta_plan_rows",
+           "proj_delta_free")
 
 
 class ProjError(RuntimeError):
@@ -58,6 +65,15 @@ class _Tactic(ctypes.Structure):
                 ("waves", ctypes.c_int), ("wpc", ctypes.c_int), ("kc", ctypes.c_int),
                 ("depth", ctypes.c_int), ("kw", ctypes.c_int), ("nw", ctypes.c_int),
                 ("stagger", ctypes.c_int)]
+
+
+class DeltaIO(ctypes.Structure):
+    """proj_delta_io_t: the operands of a call of the gated delta rule."""
+    _fields_ = ([(n, ctypes.c_void_p) for n in ("q", "k", "v", "f", "b")] +
+                [(n, ctypes.c_long) for n in ("ldq", "ldk", "ldv", "ldf", "ldb")] +
+                [(n, ctypes.c_void_p) for n in ("a_log", "dt_bias", "state", "out")] +
+                [("ldo", ctypes.c_long), ("scale", ctypes.c_float),
+                 ("l2norm", ctypes.c_int), ("head_gate", ctypes.c_int)])
 
 
 @dataclasses.dataclass(frozen=True)
@@ -76,6 +92,8 @@ class Tactic:
 
     @property
     def kernel_name(self) -> str:
+        if self.kernel == KERNEL_I8_PIPE:
+            return "i8_pipe"
         return KERNEL_NAMES.get(self.kernel, str(self.kernel))
 
     def as_dict(self) -> dict:
@@ -139,6 +157,25 @@ def _lib():
     lib.proj_run_noalloc.restype = ctypes.c_int
     lib.proj_read_probe.argtypes = [vp, ctypes.c_size_t, vp, ctypes.c_int, vp]
     lib.proj_read_probe.restype = ctypes.c_int
+    cl, cf, ip = ctypes.c_long, ctypes.c_float, ctypes.POINTER(ctypes.c_int)
+    tac, io = ctypes.POINTER(_Tactic), ctypes.POINTER(DeltaIO)
+    for name, args in (
+            ("proj_rms_norm", [ci, ci, vp, cl, vp, cl, ci, vp, cf, vp, vp, vp, vp]),
+            ("proj_quant_rows", [ci, ci, vp, cl, vp, vp, vp]),
+            ("proj_i8_plan", [ci, ci, ip, ci, ctypes.c_uint, ctypes.POINTER(vp)]),
+            ("proj_i8_run", [vp, ci, vp, cl, vp, vp, vp, vp, vp]),
+            ("proj_i8_plan_tactic", [vp, ci, tac, ip]),
+            ("proj_i8_plan_set_tactic", [vp, ci, tac]),
+            ("proj_delta_step", [io, ci, ci, ci, ci, vp, ci, vp]),
+            ("proj_delta_plan", [ci, ci, ci, ip, ip, ci, ctypes.c_uint, ctypes.POINTER(vp)]),
+            ("proj_delta_run", [vp, io, vp])):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = args, ci
+    for name, res in (("proj_i8_free", None), ("proj_delta_free", None),
+                      ("proj_i8_plan_workspace_bytes", ctypes.c_size_t),
+                      ("proj_delta_plan_rows", cl)):
+        fn = getattr(lib, name)
+        fn.argtypes, fn.restype = [vp], res
     _LIB = lib
     return lib
 
@@ -279,6 +316,19 @@ def _same_device(*tensors):
         raise ValueError("every operand must be a device tensor")
     if len({t.device for t in tensors}) != 1:
         raise ValueError("operands on different devices")
+
+
+def _on_current_device(*tensors):
+    """_same_device, and that device the current one: the calls without a plan
+    launch on the current device."""
+    import torch
+    for t in tensors:
+        if not t.is_cuda:
+            raise ValueError("every operand must be a device tensor")
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t.device.index != cur:
+            raise ValueError(f"an operand on {t.device}, the current device is cuda:{cur}")
 
 
 def run_noalloc_ptr(N: int, K: int, B: int, x_ptr: int, ldx: int, w_ptr: int, y_ptr: int,

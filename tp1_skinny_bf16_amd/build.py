@@ -1,7 +1,9 @@
 """Build the HIP library libtp1proj.so in-tree for gfx950.
 
 The library is the C ABI of include/tp1_proj.h: host plan logic (plan.cpp,
-tactics_table.cpp), the ABI (proj_abi.hip) and the kernels (kernels.hip).
+tactics_table.cpp), the ABI (proj_abi.hip) and the kernels (kernels.hip), and
+the layer operators: the norm and row codes (norm.hip), the 8-bit projection
+(proj_i8.hip) and the gated delta rule (delta_*.hip).
 All HIP code is compiled with packed-FP32 instructions disabled.
 """
 from __future__ import annotations
@@ -17,7 +19,8 @@ ROOT = os.path.dirname(PKG)
 LIB = os.path.join(PKG, "libtp1proj.so")
 ARCH = os.environ.get("TP1_OFFLOAD_ARCH", "gfx950")
 
-SOURCES = ["plan.cpp", "tactics_table.cpp", "proj_abi.hip", "kernels.hip", "probes.hip"]
+SOURCES = ["plan.cpp", "tactics_table.cpp", "proj_abi.hip", "kernels.hip", "probes.hip",
+           "norm.hip", "proj_i8.hip", "delta_abi.hip", "delta_step.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -1,0 +1,53 @@
+// delta.hpp -- the gated delta rule: the launch interface of its recurrent
+// (delta_step.hip) and chunked (delta_chunk.hip) kernels, and what a token's
+// gate is.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "../../include/tp1_proj.h"
+
+namespace tp1 {
+
+constexpr int kHead = PROJ_DELTA_HEAD;  // key and value size of a head
+
+struct DeltaArgs {
+    const uint16_t *q, *k, *v, *f, *b;  // BF16 rows
+    long ldq, ldk, ldv, ldf, ldb;       // row strides in elements
+    const float *a_log, *dt_bias;
+    float *state;                       // [n_slots][H][key][value]
+    uint16_t *out;
+    long ldo;
+    float scale;                        // of q
+    int l2norm;
+    int H, rep;                         // value heads, and how many share a key head
+    int n_slots;
+};
+
+// Which rows and which state a sequence has: from a device table of
+// {first row, rows, slot} (slots checked on the host, no two alike), or
+// request i has rows [i * tokens, (i + 1) * tokens) and slots[i].
+struct DeltaSeqs {
+    const int *table;
+    const int *slots;
+    int tokens;
+    int n;
+};
+
+hipError_t launch_delta_steps(const DeltaArgs &a, const DeltaSeqs &s, bool head_gate, int cus,
+                              hipStream_t st);
+
+#ifdef __HIPCC__
+// ln of a token's decay: -exp(A_log) * softplus(f + dt_bias).
+__device__ __forceinline__ float log_decay(float rate, float f, float bias) {
+    const float z = f + bias;
+    return -rate * (fmaxf(z, 0.f) + log1pf(expf(-fabsf(z))));
+}
+__device__ __forceinline__ float sigmoid(float x) { return 1.f / (1.f + expf(-x)); }
+// Added to a squared length before its root.
+constexpr float kUnitEps = 1e-6f;
+#endif
+
+}  // namespace tp1
