@@ -20,7 +20,7 @@ LIB = os.path.join(PKG, "libtp1proj.so")
 ARCH = os.environ.get("TP1_OFFLOAD_ARCH", "gfx950")
 
 SOURCES = ["plan.cpp", "tactics_table.cpp", "proj_abi.hip", "kernels.hip", "probes.hip",
-           "norm.hip", "proj_i8.hip", "delta_abi.hip", "delta_step.hip"]
+           "norm.hip", "proj_i8.hip", "delta_abi.hip", "delta_step.hip", "delta_chunk.hip"]
 
 HIPCC_FLAGS = [
     "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",

@@ -36,8 +36,29 @@ struct DeltaSeqs {
     int n;
 };
 
+// The chunked form.
+constexpr int kDeltaChunk = 64;             // tokens a chunk
+constexpr int kDeltaItemBytes = 123392;     // workspace of a chunk and head
+constexpr int kDeltaPrepareLds = 77056;     // LDS of a workgroup
+
+// A segment of the chunks: which to prepare, and which sequences to carry on.
+struct DeltaSegment {
+    const int *chunk_table;  // {first row, rows} a chunk, by place in the workspace
+    const int *seq_table;    // {first row, rows, slot, first chunk} a sequence
+    char *ws;
+    int chunks, seqs;
+};
+
 hipError_t launch_delta_steps(const DeltaArgs &a, const DeltaSeqs &s, bool head_gate, int cus,
                               hipStream_t st);
+
+// The scan of one segment and the preparation of the next (either may be
+// empty) in one launch; narrow: eight waves a head in the scan, not four.
+hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
+                               const DeltaSegment &prep, bool head_gate, bool narrow,
+                               hipStream_t st);
+// Allow the chunk kernels their LDS on the current device.
+hipError_t allow_delta_lds();
 
 #ifdef __HIPCC__
 // ln of a token's decay: -exp(A_log) * softplus(f + dt_bias).

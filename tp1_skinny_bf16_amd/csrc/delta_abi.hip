@@ -4,6 +4,7 @@
 
 #include <algorithm>
 #include <cstdint>
+#include <mutex>
 #include <new>
 #include <vector>
 
@@ -15,7 +16,10 @@ struct proj_delta_plan_s {
     int H = 0, Hk = 0, n = 0, n_slots = 0, device = -1, cus = 256;
     long rows = 0;               // of all sequences together
     unsigned flags = 0;
-    int *table = nullptr;        // device: {first row, rows, slot} a sequence
+    int shorts = 0;              // sequences that run token by token
+    std::vector<tp1::DeltaSegment> segments;
+    void *mem = nullptr;         // device: tables, then two workspaces
+    const int *short_table = nullptr;
 };
 
 namespace tp1 {
@@ -58,6 +62,128 @@ int check_io(const proj_delta_io_t *io, int H, int Hk, long rows, int n_slots, D
     if (out.meets(state)) return PROJ_EINVAL;
     for (const Span &s : in)
         if (out.meets(s) || state.meets(s)) return PROJ_EINVAL;
+    return PROJ_OK;
+}
+
+// A sequence of at most this many rows runs token by token: a chunk costs
+// about as much however few of its 64 tokens there are.
+constexpr int kShortRows = 16;
+
+// Chunks and heads a segment prepares at a time: enough workgroups to fill
+// the device, and two workspaces that stay inside the memory-side cache.
+constexpr long kSegmentItems = 1024;
+
+struct Tables {
+    std::vector<int> words;                 // every table, one after another
+    std::vector<tp1::DeltaSegment> segments;
+    std::vector<size_t> chunk_at, seq_at;   // where a segment's tables start
+    int shorts = 0, most = 0;               // most chunks of a segment
+};
+
+// Cuts the sequences' chunks into segments, first chunks of all sequences
+// first, so that every segment carries many sequences on.
+Tables cut(int H, int n, const int *lens, const int *slots) {
+    Tables t;
+    std::vector<long> row(n);
+    long r = 0;
+    for (int i = 0; i < n; ++i) {
+        row[i] = r;
+        r += lens[i];
+        if (lens[i] > 0 && lens[i] <= kShortRows) {
+            t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
+            ++t.shorts;
+        }
+    }
+    const int per = (int)std::max(1L, kSegmentItems / H);
+    struct Chunk {
+        int seq, at;
+    };
+    std::vector<Chunk> seg;
+    auto close = [&]() {
+        if (seg.empty()) return;
+        std::stable_sort(seg.begin(), seg.end(),
+                         [](const Chunk &x, const Chunk &y) { return x.seq < y.seq; });
+        DeltaSegment s{};
+        s.chunks = (int)seg.size();
+        t.chunk_at.push_back(t.words.size());
+        for (const Chunk &c : seg) {
+            t.words.push_back((int)(row[c.seq] + (long)c.at * kDeltaChunk));
+            t.words.push_back(std::min(kDeltaChunk, lens[c.seq] - c.at * kDeltaChunk));
+        }
+        t.seq_at.push_back(t.words.size());
+        for (size_t i = 0; i < seg.size();) {
+            size_t j = i;
+            while (j < seg.size() && seg[j].seq == seg[i].seq) ++j;
+            const Chunk &a = seg[i], &b = seg[j - 1];
+            const int end = std::min(lens[a.seq], (b.at + 1) * kDeltaChunk);
+            t.words.insert(t.words.end(), {(int)(row[a.seq] + (long)a.at * kDeltaChunk),
+                                           end - a.at * kDeltaChunk, slots[a.seq], (int)i});
+            ++s.seqs;
+            i = j;
+        }
+        t.most = std::max(t.most, s.chunks);
+        t.segments.push_back(s);
+        seg.clear();
+    };
+    std::vector<int> left;                  // sequences with chunks still to place
+    for (int i = 0; i < n; ++i)
+        if (lens[i] > kShortRows) left.push_back(i);
+    for (int at = 0; !left.empty(); ++at) {
+        size_t keep = 0;
+        for (const int i : left) {
+            seg.push_back({i, at});
+            if ((int)seg.size() == per) close();
+            if (lens[i] - at * kDeltaChunk > kDeltaChunk) left[keep++] = i;
+        }
+        left.resize(keep);
+    }
+    close();
+    return t;
+}
+
+int prepare_delta(int dev) {
+    static std::mutex mu;
+    static bool done[64] = {};
+    std::lock_guard<std::mutex> lock(mu);
+    if (dev >= 0 && dev < 64 && done[dev]) return PROJ_OK;
+    if (allow_delta_lds() != hipSuccess) {
+        (void)hipGetLastError();
+        return PROJ_EHIP;
+    }
+    if (dev >= 0 && dev < 64) done[dev] = true;
+    return PROJ_OK;
+}
+
+// Tables and two workspaces on the current device.
+int place(proj_delta_plan_s *p, Tables &t) {
+    int dev = -1, cus = 0;
+    if (hipGetDevice(&dev) != hipSuccess ||
+        hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
+        return PROJ_EHIP;
+    p->device = dev;
+    if (cus > 0) p->cus = cus;
+    const int rc = prepare_delta(dev);
+    if (rc != PROJ_OK) return rc;
+    const size_t words = t.words.size() * sizeof(int);
+    const size_t tables = (words + 255) / 256 * 256;
+    const size_t ws = (size_t)t.most * p->H * kDeltaItemBytes;
+    const size_t bytes = tables + ws * std::min<size_t>(2, t.segments.size());
+    if (bytes == 0) return PROJ_OK;
+    if (hipMalloc(&p->mem, bytes) != hipSuccess) {
+        p->mem = nullptr;
+        return PROJ_ENOMEM;
+    }
+    if (hipMemcpy(p->mem, t.words.data(), words, hipMemcpyHostToDevice) != hipSuccess)
+        return PROJ_EHIP;
+    const int *w = static_cast<const int *>(p->mem);
+    p->shorts = t.shorts;
+    p->short_table = w;
+    for (size_t i = 0; i < t.segments.size(); ++i) {
+        t.segments[i].chunk_table = w + t.chunk_at[i];
+        t.segments[i].seq_table = w + t.seq_at[i];
+        t.segments[i].ws = static_cast<char *>(p->mem) + tables + (i & 1) * ws;
+    }
+    p->segments.swap(t.segments);
     return PROJ_OK;
 }
 
@@ -115,50 +241,26 @@ int proj_delta_plan(int heads, int qk_heads, int n, const int *lens, const int *
             if (slots[j] == slots[i]) return PROJ_EINVAL;  // one state, one sequence
     }
     if (rows > PROJ_DELTA_MAX_ROWS) return PROJ_EINVAL;
-    proj_delta_plan_s *p = new (std::nothrow) proj_delta_plan_s;
-    int *host = new (std::nothrow) int[3 * (size_t)n];
-    if (!p || !host) {
-        delete p;
-        delete[] host;
-        return PROJ_ENOMEM;
-    }
-    p->H = heads;
-    p->Hk = qk_heads;
-    p->n = n;
-    p->n_slots = n_slots;
-    p->rows = rows;
-    p->flags = flags;
-    long r = 0;
-    for (int i = 0; i < n; ++i) {
-        host[3 * i] = (int)r;
-        host[3 * i + 1] = lens[i];
-        host[3 * i + 2] = slots[i];
-        r += lens[i];
-    }
+    proj_delta_plan_s *p = nullptr;
     int rc = PROJ_OK;
-    if (!(flags & PROJ_PLAN_HOST_ONLY)) {
-        int dev = -1, cus = 0;
-        void *mem = nullptr;
-        const size_t bytes = 3 * (size_t)n * sizeof(int);
-        if (hipGetDevice(&dev) != hipSuccess ||
-            hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess)
-            rc = PROJ_EHIP;
-        else if (hipMalloc(&mem, bytes) != hipSuccess)
-            rc = PROJ_ENOMEM;
-        else if (hipMemcpy(mem, host, bytes, hipMemcpyHostToDevice) != hipSuccess)
-            rc = PROJ_EHIP;
-        if (rc != PROJ_OK) {
-            (void)hipGetLastError();
-            if (mem) (void)hipFree(mem);
-        } else {
-            p->device = dev;
-            if (cus > 0) p->cus = cus;
-            p->table = static_cast<int *>(mem);
+    try {
+        p = new proj_delta_plan_s;
+        p->H = heads;
+        p->Hk = qk_heads;
+        p->n = n;
+        p->n_slots = n_slots;
+        p->rows = rows;
+        p->flags = flags;
+        if (!(flags & PROJ_PLAN_HOST_ONLY)) {
+            Tables t = cut(heads, n, lens, slots);
+            rc = place(p, t);
         }
+    } catch (const std::bad_alloc &) {
+        rc = PROJ_ENOMEM;
     }
-    delete[] host;
     if (rc != PROJ_OK) {
-        delete p;
+        (void)hipGetLastError();
+        proj_delta_free(p);
         return rc;
     }
     *out = p;
@@ -167,11 +269,11 @@ int proj_delta_plan(int heads, int qk_heads, int n, const int *lens, const int *
 
 void proj_delta_free(proj_delta_plan_t *p) {
     if (!p) return;
-    if (p->table) {
+    if (p->mem) {
         int cur = -1;
         const bool other = hipGetDevice(&cur) == hipSuccess && cur != p->device;
         if (other) (void)hipSetDevice(p->device);
-        (void)hipFree(p->table);
+        (void)hipFree(p->mem);
         if (other) (void)hipSetDevice(cur);
     }
     delete p;
@@ -190,8 +292,20 @@ int proj_delta_run(const proj_delta_plan_t *p, const proj_delta_io_t *io, void *
     int cur = -1;
     if (hipGetDevice(&cur) != hipSuccess || cur != p->device) return PROJ_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
-    const DeltaSeqs s{p->table, nullptr, 0, p->n};
-    if (launch_delta_steps(a, s, io->head_gate, p->cus, st) != hipSuccess) {
+    hipError_t e = hipSuccess;
+    if (p->shorts) {
+        const DeltaSeqs s{p->short_table, nullptr, 0, p->shorts};
+        e = launch_delta_steps(a, s, io->head_gate, p->cus, st);
+    }
+    // segment i's scan shares a launch with segment i + 1's preparation
+    const size_t n = p->segments.size();
+    for (size_t i = 0; n && i <= n && e == hipSuccess; ++i) {
+        const DeltaSegment none{};
+        const DeltaSegment &scan = i ? p->segments[i - 1] : none;
+        const DeltaSegment &prep = i < n ? p->segments[i] : none;
+        e = launch_delta_chunks(a, scan, prep, io->head_gate, true, st);
+    }
+    if (e != hipSuccess) {
         (void)hipGetLastError();
         return PROJ_EHIP;
     }

@@ -1,0 +1,736 @@
+// delta_chunk.hip -- the gated delta rule over sequences, 64 tokens at a time.
+//
+// Write G_i for the sum of the log decays of a chunk's tokens up to and with
+// token i (a vector over the 128 key channels), S for the state before the
+// chunk, and u_i for what token i adds (S <- S + k_i u_i^T).  Unrolling the
+// recurrence inside the chunk,
+//     u_i = beta_i (v_i - S^T (k_i e^{G_i}) - sum_{j<i} A_ij u_j),
+//     A_ij = sum_c k_ic k_jc e^{G_ic - G_jc},
+//     o_i = S^T (q_i e^{G_i}) + sum_{j<=i} P_ij u_j,   P_ij as A with q_i,
+//     S'  = diag(e^{G_64}) S + sum_j (k_j e^{G_64 - G_j}) u_j^T.
+// With N = diag(beta) A (strictly lower triangular) and T = (1 + N)^-1
+// diag(beta), the u_i are U = T V - (T K e^G) S.  Everything but the terms
+// in S is independent of the chunks before, so the work is in two parts:
+//   prepare (one workgroup a chunk and head): W = -T K e^G, U0 = T V, P,
+//     Q e^G, K e^{G_64 - G} and e^{G_64}, written to a workspace;
+//   scan (four waves a head, 32 columns of the state each, or eight of 16):
+//     chunk after chunk, U = U0 + W S, O = (Q e^G) S + P U, S' as above.
+//
+// Numbers.  All products run on the bf16 matrix cores with FP32 sums.  What
+// reaches the state (W, U, K, S as operands) is split into two bf16 values
+// hi + lo, and hi hi + hi lo + lo hi are summed: 2^-17 of each value is
+// lost, where one bf16 rounding would lose 2^-9 of the state a chunk.  What
+// only reaches the BF16 output (Q, P) is one bf16 value against a split one.
+// Decays are products of factors e^x with x <= 0, the sums x taken inside
+// blocks of 16 tokens from the token outward, so none is a difference of
+// large numbers: with block a after block b, e^{G_i - G_j} = (e^{sum of a's
+// tokens up to i}) (e^{whole blocks between}) (e^{sum of b's tokens after
+// j}).  Inside a block the second factor is e^{-(sum up to j)} instead,
+// which grows: a block whose tokens decay a channel by more than e^-40 takes
+// an exact path on the vector unit (a running sum from i down to j).  A
+// token's log decay is held above -120 (e^-120 is 0 in FP32), so that
+// infinite gates make no NaN.
+//
+// Layout.  A wave of `prepare` owns one block of 16 tokens; lane l holds
+// token l % 16 and, for s = 0..3, channels 32 s + 8 (l / 16) + 0..7, which is
+// the A and B operand of v_mfma_f32_16x16x32_bf16 over channels.  Sums over
+// the tokens of a block are scans over 16 lanes (DPP).  Operands over tokens
+// need the transpose, which a product with a selection matrix gives exactly
+// (accumulator lane l holds rows 4 (l / 16) + 0..3 of column l % 16).  The
+// order of the 32 summed values of a product is free, so the scan feeds its
+// accumulators S and U back as operands without any exchange: S tile 2 s + h
+// has channel 32 s + 8 (r / 4) + 4 h + r % 4 as row r, and a step over tokens
+// takes blocks 2 t and 2 t + 1, tokens 4 (l / 16) + 0..3 of each.  The
+// workspace holds every operand in that order, so each load is 16 bytes a
+// lane, 1 KB in one piece.
+#include "delta.hpp"
+
+#include "device.hpp"
+
+namespace tp1 {
+
+namespace {
+
+constexpr int kC = kDeltaChunk;   // tokens a chunk
+
+// Workspace of a chunk and head, in bytes.
+constexpr int kWsW = 0;                       // [4 token tiles][4 s][hi, lo][64][16]
+constexpr int kWsQ = kWsW + 32768;            // [4][4 s][64][16]
+constexpr int kWsK = kWsQ + 16384;            // [8 channel tiles][2 steps][hi, lo][64][16]
+constexpr int kWsP = kWsK + 32768;            // [4][2 steps][64][16]
+constexpr int kWsU = kWsP + 8192;             // [4][8 value tiles][64][16]
+constexpr int kWsD = kWsU + 32768;            // [128] FP32
+static_assert(kWsD + 512 == kDeltaItemBytes, "workspace of an item");
+
+// LDS of `prepare`, in bytes.
+constexpr int kLdsKr = 0;                     // [hi, lo][48 rows][256], dead after barrier 2
+constexpr int kLdsT = 0;                      // [hi, lo][10 blocks][16 rows][40]
+constexpr int kLdsV = kLdsT + 2 * 10 * 640;   // [8 value tiles][2 steps][64][16]
+constexpr int kLdsK = kLdsV + 16384;          // [8 channel tiles][2 steps][hi, lo][64][16]
+constexpr int kLdsN = kLdsK + 32768;          // [10 blocks][16 rows][20] FP32
+constexpr int kLdsTot = kLdsN + 10 * 1280;    // [4][128] FP32
+constexpr int kLdsBeta = kLdsTot + 2048;      // [64] FP32
+static_assert(kLdsKr + 2 * 48 * 256 <= kLdsK, "the transposed values reuse the key rows");
+static_assert(kLdsBeta + 256 == kDeltaPrepareLds, "LDS of prepare");
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
+                                                   __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
+}
+
+// e^x for x in [-8000, 88]: 2^(x log2 e) with the product's rounding error
+// put back to first order.
+__device__ __forceinline__ float exp_of(float x) {
+    const float t = x * 1.442695041f;
+    float r = __builtin_fmaf(x, 1.442695041f, -t);
+    r = __builtin_fmaf(x, 1.92596299e-8f, r);  // log2 e beyond its FP32 value
+    const float e = __builtin_amdgcn_exp2f(t);
+    return __builtin_fmaf(e, r * 0.6931472f, e);
+}
+
+// ln(1 + e^z) = max(z, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|z|; the
+// series in s^2 <= 1/9 stops below 2^-25 of the value.
+__device__ __forceinline__ float softplus_of(float z) {
+    const float e = exp_of(-fminf(fabsf(z), 200.f));
+    const float s = e * __builtin_amdgcn_rcpf(2.f + e), t = s * s;
+    float p = 1.f / 13.f;
+    p = __builtin_fmaf(p, t, 1.f / 11.f);
+    p = __builtin_fmaf(p, t, 1.f / 9.f);
+    p = __builtin_fmaf(p, t, 1.f / 7.f);
+    p = __builtin_fmaf(p, t, 1.f / 5.f);
+    p = __builtin_fmaf(p, t, 1.f / 3.f);
+    p = __builtin_fmaf(p, t, 1.f);
+    const float r = fmaxf(z, 0.f) + 2.f * s * p;
+    return z == z ? r : z;
+}
+
+// A token's log decay, held above -120.
+__device__ __forceinline__ float gate_of(float rate, float f, float bias) {
+    const float g = -rate * softplus_of(f + bias);
+    return g < -120.f ? -120.f : g;
+}
+
+struct Split {
+    u32x4 hi, lo;
+};
+// Eight values as bf16 pairs hi + lo.
+__device__ __forceinline__ Split split8(const float *x) {
+    Split o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const unsigned h = pack_bf16(x[2 * i], x[2 * i + 1]);
+        o.hi[i] = h;
+        o.lo[i] = pack_bf16(x[2 * i] - bf16_lo(h), x[2 * i + 1] - bf16_hi(h));
+    }
+    return o;
+}
+__device__ __forceinline__ Split split8(f32x4 a, f32x4 b) {
+    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    return split8(x);
+}
+__device__ __forceinline__ u32x2 pack4(f32x4 a) {
+    return u32x2{pack_bf16(a.x, a.y), pack_bf16(a.z, a.w)};
+}
+__device__ __forceinline__ void unpack8(u32x4 v, float *x) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        x[2 * i] = bf16_lo(v[i]);
+        x[2 * i + 1] = bf16_hi(v[i]);
+    }
+}
+
+// Place of block (a, b), b <= a, among the lower triangle's ten.
+__device__ __forceinline__ int block_of(int a, int b) { return a * (a + 1) / 2 + b; }
+
+// Orders this wave's LDS writes before its later reads by other lanes.
+__device__ __forceinline__ void wave_sync() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+}
+
+// Sums over the lanes of a 16-lane row: up to and with this one, and after it.
+__device__ __forceinline__ float sum_upto(float v) {
+    v += dpp_move<0x111>(v);
+    v += dpp_move<0x112>(v);
+    v += dpp_move<0x114>(v);
+    v += dpp_move<0x118>(v);
+    return v;
+}
+__device__ __forceinline__ float sum_after(float v) {
+    v += dpp_move<0x101>(v);
+    v += dpp_move<0x102>(v);
+    v += dpp_move<0x104>(v);
+    v += dpp_move<0x108>(v);
+    return dpp_move<0x101>(v);
+}
+
+// ---------------------------------------------------------------------------
+// prepare: one workgroup of four waves a chunk and head.
+// ---------------------------------------------------------------------------
+template <bool HEAD_GATE>
+__device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n, int h, char *ws,
+                                             char *lds) {
+    const int lane = threadIdx.x & 63;
+    const int w = scalar(threadIdx.x >> 6);
+    const int lr = lane & 15, lg = lane >> 4;
+    const int hk = h / a.rep;
+    const bool live = w * 16 + lr < n;
+    const long row = row0 + w * 16 + lr;
+    float *tot = reinterpret_cast<float *>(lds + kLdsTot);
+    float *betas = reinterpret_cast<float *>(lds + kLdsBeta);
+    float *Nb = reinterpret_cast<float *>(lds + kLdsN);
+
+    // ---- this lane's token: keys, queries, values, gates
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    u32x4 kv[4], qv[4], vv[4], fv[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int c = 32 * s + 8 * lg;
+        kv[s] = qv[s] = vv[s] = fv[s] = zero;
+        if (live) {
+            kv[s] = *reinterpret_cast<const u32x4 *>(a.k + row * a.ldk + hk * kHead + c);
+            qv[s] = *reinterpret_cast<const u32x4 *>(a.q + row * a.ldq + hk * kHead + c);
+            vv[s] = *reinterpret_cast<const u32x4 *>(a.v + row * a.ldv + h * kHead + c);
+            if constexpr (!HEAD_GATE)
+                fv[s] = *reinterpret_cast<const u32x4 *>(a.f + row * a.ldf + h * kHead + c);
+        }
+    }
+    float rk = 1.f, rq = a.scale;
+    if (a.l2norm) {
+        float sk = 0.f, sq = 0.f;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float k0 = bf16_lo(kv[s][i]), k1 = bf16_hi(kv[s][i]);
+                const float q0 = bf16_lo(qv[s][i]), q1 = bf16_hi(qv[s][i]);
+                sk = __builtin_fmaf(k0, k0, __builtin_fmaf(k1, k1, sk));
+                sq = __builtin_fmaf(q0, q0, __builtin_fmaf(q1, q1, sq));
+            }
+        sk += __shfl_xor(sk, 16);
+        sq += __shfl_xor(sq, 16);
+        sk += __shfl_xor(sk, 32);
+        sq += __shfl_xor(sq, 32);
+        rk = rsqrtf(sk + kUnitEps);
+        rq *= rsqrtf(sq + kUnitEps);
+    }
+    const float rate = expf(a.a_log[h]);
+    if (lg == 0) betas[w * 16 + lr] = live ? sigmoid(bf16_value(a.b[row * a.ldb + h])) : 0.f;
+
+    float el[4][8], er[4][8], g[4][8];  // e^{sum up to}, e^{sum after}, log decay
+    bool mild = true;
+    if constexpr (HEAD_GATE) {
+        const float gt = live ? gate_of(rate, bf16_value(a.f[row * a.ldf + h]), a.dt_bias[h]) : 0.f;
+        const float up = sum_upto(gt), after = sum_after(gt);
+        const float eu = exp_of(up), ea = exp_of(after);
+        mild = !(up < -40.f);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) g[s][e] = gt, el[s][e] = eu, er[s][e] = ea;
+            if (lr == 15) {
+                f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + 32 * s + 8 * lg);
+                t[0] = t[1] = f32x4{up, up, up, up};
+            }
+        }
+    } else {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            const int c = 32 * s + 8 * lg;
+            float bias[8], up[8];
+            const f32x4 *bp = reinterpret_cast<const f32x4 *>(a.dt_bias + h * kHead + c);
+            *reinterpret_cast<f32x4 *>(bias) = bp[0];
+            *reinterpret_cast<f32x4 *>(bias + 4) = bp[1];
+            unpack8(fv[s], g[s]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                g[s][e] = live ? gate_of(rate, g[s][e], bias[e]) : 0.f;
+                up[e] = sum_upto(g[s][e]);
+                mild = mild && !(up[e] < -40.f);
+                el[s][e] = exp_of(up[e]);
+                er[s][e] = exp_of(sum_after(g[s][e]));
+            }
+            if (lr == 15) {
+                f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + c);
+                t[0] = f32x4{up[0], up[1], up[2], up[3]};
+                t[1] = f32x4{up[4], up[5], up[6], up[7]};
+            }
+        }
+    }
+    mild = __all(mild);
+
+    // ---- keys scaled to the end of their block, for the blocks after
+    float kf[4][8], qf[4][8];
+    Split kl[4];   // k e^{sum up to}
+    u32x4 ql[4];   // q e^{sum up to}, one bf16 value
+    float krf[4][8];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        unpack8(kv[s], kf[s]);
+        unpack8(qv[s], qf[s]);
+        float x[8], y[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            kf[s][e] *= rk;
+            qf[s][e] *= rq;
+            x[e] = kf[s][e] * el[s][e];
+            y[e] = qf[s][e] * el[s][e];
+            krf[s][e] = kf[s][e] * er[s][e];
+        }
+        kl[s] = split8(x);
+        ql[s] = split8(y).hi;
+        if (w < 3) {
+            const Split r = split8(krf[s]);
+            const int j = w * 16 + lr, p = (4 * s + lg) ^ lr;
+            *reinterpret_cast<u32x4 *>(lds + kLdsKr + j * 256 + p * 16) = r.hi;
+            *reinterpret_cast<u32x4 *>(lds + kLdsKr + 48 * 256 + j * 256 + p * 16) = r.lo;
+        }
+    }
+    __syncthreads();  // 1: key rows, block totals and betas are there
+
+    // ---- to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+        const int c = 32 * s + 8 * lg;
+        float before[8], behind[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) before[e] = behind[e] = 0.f;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) {
+            const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c);
+            const f32x4 t1 = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                before[e] += b < w ? t0[e] : 0.f;
+                before[e + 4] += b < w ? t1[e] : 0.f;
+                behind[e] += b > w ? t0[e] : 0.f;
+                behind[e + 4] += b > w ? t1[e] : 0.f;
+            }
+        }
+        float kt[8], kh[8], qt[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float f = exp_of(before[e]);
+            kt[e] = kf[s][e] * el[s][e] * f;
+            qt[e] = qf[s][e] * el[s][e] * f;
+            kh[e] = krf[s][e] * exp_of(behind[e]);
+        }
+        *reinterpret_cast<u32x4 *>(ws + kWsQ + ((w * 4 + s) * 64 + lane) * 16) = split8(qt).hi;
+        const Split st = split8(kt), sh = split8(kh);
+        if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
+            float d[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) d[e] = el[s][e] * exp_of(before[e]);
+            f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
+            o[0] = f32x4{d[0], d[1], d[2], d[3]};
+            o[1] = f32x4{d[4], d[5], d[6], d[7]};
+        }
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            // column r of the selection picks channel 8 (r / 4) + 4 hf + r % 4
+            u32x4 sel = zero;
+            if (lg == lr >> 2) {
+                const int e = (lr & 3) + 4 * hf;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
+            }
+            const int at = ((2 * s + hf) * 2 + (w >> 1)) * 2048 + lane * 16 + (w & 1) * 8;
+            *reinterpret_cast<u32x2 *>(lds + kLdsK + at) = pack4(mfma(st.hi, sel, none));
+            *reinterpret_cast<u32x2 *>(lds + kLdsK + at + 1024) = pack4(mfma(st.lo, sel, none));
+            *reinterpret_cast<u32x2 *>(ws + kWsK + at) = pack4(mfma(sh.hi, sel, none));
+            *reinterpret_cast<u32x2 *>(ws + kWsK + at + 1024) = pack4(mfma(sh.lo, sel, none));
+        }
+    }
+
+    // ---- A (times beta, to LDS) and P (to the workspace), block row w
+    const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4);
+    for (int b = 0; b <= w; ++b) {
+        f32x4 A = none, P = none;  // A[i = 4 lg + r][j = lr], P[j = 4 lg + r][i = lr]
+        if (b < w || mild) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                Split r;
+                if (b == w) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        // e^{-(sum up to j)}; el is at least e^-40 here
+                        x[e] = kf[s][e] / el[s][e];
+                    }
+                    r = split8(x);
+                } else {
+                    const int p = (4 * s + lg) ^ lr;
+                    const char *at = lds + kLdsKr + (b * 16 + lr) * 256 + p * 16;
+                    r.hi = *reinterpret_cast<const u32x4 *>(at);
+                    r.lo = *reinterpret_cast<const u32x4 *>(at + 48 * 256);
+                    if (w - b > 1) {  // whole blocks between
+                        float x[8], y[8], m[8];
+                        unpack8(r.hi, x);
+                        unpack8(r.lo, y);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) m[e] = 0.f;
+                        for (int o = b + 1; o < w; ++o) {
+                            const float *t = tot + o * kHead + 32 * s + 8 * lg;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) m[e] += t[e];
+                        }
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) x[e] = (x[e] + y[e]) * exp_of(m[e]);
+                        r = split8(x);
+                    }
+                }
+                A = mfma(kl[s].hi, r.hi, A);
+                A = mfma(kl[s].hi, r.lo, A);
+                A = mfma(kl[s].lo, r.hi, A);
+                P = mfma(r.hi, ql[s], P);
+                P = mfma(r.lo, ql[s], P);
+            }
+        } else {
+            // Exact inside a block: for d = 1..15, token i with j = i - d, the
+            // decay's exponent summed from i down.  Lane l holds i = l % 16.
+            float gs[4][8], ks[4][8], x[4][8];
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gs[s][e] = g[s][e], ks[s][e] = kf[s][e], x[s][e] = 0.f;
+            float *blk = Nb + block_of(w, w) * 320;
+            float pi[16], ai[16];  // row i of P and A, by distance
+#pragma unroll
+            for (int d = 0; d < 16; ++d) {
+                float pa = 0.f, pp = 0.f;
+#pragma unroll
+                for (int s = 0; s < 4; ++s)
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        if (d > 0) {
+                            x[s][e] += gs[s][e];  // of token i - d + 1
+                            gs[s][e] = dpp_move<0x111>(gs[s][e]);
+                            ks[s][e] = dpp_move<0x111>(ks[s][e]);
+                        }
+                        const float y = ks[s][e] * exp_of(x[s][e]);
+                        pa = __builtin_fmaf(kf[s][e], y, pa);
+                        pp = __builtin_fmaf(qf[s][e], y, pp);
+                    }
+                pa += __shfl_xor(pa, 16);
+                pp += __shfl_xor(pp, 16);
+                ai[d] = pa + __shfl_xor(pa, 32);
+                pi[d] = pp + __shfl_xor(pp, 32);
+            }
+            // through LDS (this wave's own block) into the accumulators' order
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+                if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = pi[d];
+            wave_sync();
+#pragma unroll
+            for (int r = 0; r < 4; ++r) P[r] = 4 * lg + r <= lr ? blk[lr * 20 + 4 * lg + r] : 0.f;
+            wave_sync();
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+                if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = ai[d];
+            wave_sync();
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                A[r] = lr <= 4 * lg + r ? blk[(4 * lg + r) * 20 + lr] : 0.f;
+            wave_sync();
+        }
+        float *blk = Nb + block_of(w, b) * 320;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (b == w && 4 * lg + r <= lr) A[r] = 0.f;  // strictly below the diagonal
+            if (b == w && 4 * lg + r > lr) P[r] = 0.f;   // on it and below
+            blk[(4 * lg + r) * 20 + lr] = A[r] * beta4[r];
+        }
+        char *po = ws + kWsP + ((w * 2 + (b >> 1)) * 64 + lane) * 16;
+        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4(P);
+        if (b == w && (w & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
+    }
+    // ---- inverse of this block's 1 + N by forward substitution, a column a lane
+    {
+        wave_sync();
+        float *blk = Nb + block_of(w, w) * 320;
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            float acc = i == lr ? 1.f : 0.f;
+#pragma unroll
+            for (int j = 0; j < i; ++j) acc = __builtin_fmaf(-blk[i * 20 + j], x[j], acc);
+            x[i] = acc;
+        }
+        wave_sync();
+        if (lg == 0)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) blk[i * 20 + lr] = x[i];
+    }
+    __syncthreads();  // 2: N below the diagonal and the inverses are there; key rows are free
+
+    // ---- V transposed, and column block w of the whole inverse
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            u32x4 sel = zero;  // column r picks value 16 hf + r
+            const int e = 16 * hf + lr - 8 * lg;
+            if (e >= 0 && e < 8)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
+            *reinterpret_cast<u32x2 *>(lds + kLdsV + ((2 * s + hf) * 2 + (w >> 1)) * 1024 +
+                                       lane * 16 + (w & 1) * 8) = pack4(mfma(vv[s], sel, none));
+        }
+    {
+        const float bj = betas[w * 16 + lr];
+        f32x4 T[4];
+        auto store_t = [&](int ai, f32x4 t) {  // T_ab diag(beta), rows i = 4 lg + r, column lr
+            char *o = lds + kLdsT + block_of(ai, w) * 640 + lr * 2;
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float x = t[r] * bj;
+                const uint16_t hi = round_bf16(x);
+                *reinterpret_cast<uint16_t *>(o + (4 * lg + r) * 40) = hi;
+                *reinterpret_cast<uint16_t *>(o + 6400 + (4 * lg + r) * 40) =
+                    round_bf16(x - bf16_value(hi));
+            }
+        };
+        const float *d = Nb + block_of(w, w) * 320;
+        f32x4 t;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] = d[(4 * lg + r) * 20 + lr];
+        store_t(w, t);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) T[i] = none;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i == w) T[i] = t;
+#pragma unroll
+        for (int i = 1; i < 4; ++i) {
+            if (i <= w) continue;  // uniform
+            f32x4 X = none;
+#pragma unroll
+            for (int c = 0; c < 3; ++c) {
+                if (c < w || c >= i) continue;
+                const f32x4 nv =
+                    *reinterpret_cast<const f32x4 *>(Nb + block_of(i, c) * 320 + lr * 20 + lg * 4);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    X = __builtin_amdgcn_mfma_f32_16x16x4f32(nv[r], T[c][r], X, 0, 0, 0);
+            }
+            const f32x4 dv =
+                *reinterpret_cast<const f32x4 *>(Nb + block_of(i, i) * 320 + lr * 20 + lg * 4);
+            f32x4 Y = none;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                Y = __builtin_amdgcn_mfma_f32_16x16x4f32(dv[r], -X[r], Y, 0, 0, 0);
+            T[i] = Y;
+            store_t(i, Y);
+        }
+    }
+    __syncthreads();  // 3: T and the transposed values are there
+
+    // ---- W = -T K e^G (channels 32 w + 0..31) and U0 = T V (the same columns)
+    f32x4 Wt[2][4], U[4][2];  // W^T[channel tile][token tile], U0[token tile][value tile]
+#pragma unroll
+    for (int it = 0; it < 4; ++it) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) Wt[hf][it] = U[it][hf] = none;
+#pragma unroll
+        for (int st = 0; st <= it >> 1; ++st) {
+            const char *t0 = lds + kLdsT + block_of(it, 2 * st) * 640 + lr * 40 + lg * 8;
+            const u32x2 h0 = *reinterpret_cast<const u32x2 *>(t0);
+            const u32x2 l0 = *reinterpret_cast<const u32x2 *>(t0 + 6400);
+            u32x2 h1 = {0u, 0u}, l1 = {0u, 0u};
+            if (2 * st + 1 <= it) {
+                h1 = *reinterpret_cast<const u32x2 *>(t0 + 640);
+                l1 = *reinterpret_cast<const u32x2 *>(t0 + 640 + 6400);
+            }
+            const u32x4 th = {h0.x, h0.y, h1.x, h1.y}, tl = {l0.x, l0.y, l1.x, l1.y};
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                const char *kp = lds + kLdsK + ((2 * w + hf) * 2 + st) * 2048 + lane * 16;
+                const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
+                const u32x4 ko = *reinterpret_cast<const u32x4 *>(kp + 1024);
+                const u32x4 vt = *reinterpret_cast<const u32x4 *>(
+                    lds + kLdsV + ((2 * w + hf) * 2 + st) * 1024 + lane * 16);
+                Wt[hf][it] = mfma(kh, th, Wt[hf][it]);
+                Wt[hf][it] = mfma(kh, tl, Wt[hf][it]);
+                Wt[hf][it] = mfma(ko, th, Wt[hf][it]);
+                U[it][hf] = mfma(th, vt, U[it][hf]);
+                U[it][hf] = mfma(tl, vt, U[it][hf]);
+            }
+        }
+        const Split o = split8(-Wt[0][it], -Wt[1][it]);
+        char *wp = ws + kWsW + ((it * 4 + w) * 2 * 64 + lane) * 16;
+        *reinterpret_cast<u32x4 *>(wp) = o.hi;
+        *reinterpret_cast<u32x4 *>(wp + 1024) = o.lo;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+            *reinterpret_cast<f32x4 *>(ws + kWsU + ((it * 8 + 2 * w + hf) * 64 + lane) * 16) =
+                U[it][hf];
+    }
+}
+
+// ---------------------------------------------------------------------------
+// scan: one wave a head and VT * 16 columns of its state, chunk after chunk.
+// ---------------------------------------------------------------------------
+template <int VT>
+__device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot,
+                                             int h, int vt0, const char *ws, size_t ws_step) {
+    const int lane = threadIdx.x & 63;
+    const int lr = lane & 15, lg = lane >> 4;
+    float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) + vt0 * 16 + lr;
+    f32x4 S[8][VT];
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int v = 0; v < VT; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                S[t][v][r] =
+                    state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead + v * 16];
+
+    for (int r0 = 0; r0 < rows; r0 += kC, ws += ws_step) {
+        const int n = min(kC, rows - r0);
+        const char *at = ws + lane * 16;
+        f32x4 U[4][VT], O[4][VT];  // U[token][value], O[value][token] (transposed)
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int v = 0; v < VT; ++v) {
+                U[it][v] = *reinterpret_cast<const f32x4 *>(at + kWsU + (it * 8 + vt0 + v) * 1024);
+                O[it][v] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            Split b[VT];
+#pragma unroll
+            for (int v = 0; v < VT; ++v) b[v] = split8(S[2 * s][v], S[2 * s + 1][v]);
+#pragma unroll
+            for (int it = 0; it < 4; ++it) {
+                const char *wp = at + kWsW + (it * 4 + s) * 2048;
+                const u32x4 wh = *reinterpret_cast<const u32x4 *>(wp);
+                const u32x4 wl = *reinterpret_cast<const u32x4 *>(wp + 1024);
+                const u32x4 q = *reinterpret_cast<const u32x4 *>(at + kWsQ + (it * 4 + s) * 1024);
+#pragma unroll
+                for (int v = 0; v < VT; ++v) {
+                    U[it][v] = mfma(wh, b[v].hi, U[it][v]);
+                    U[it][v] = mfma(wh, b[v].lo, U[it][v]);
+                    U[it][v] = mfma(wl, b[v].hi, U[it][v]);
+                    O[it][v] = mfma(b[v].hi, q, O[it][v]);
+                    O[it][v] = mfma(b[v].lo, q, O[it][v]);
+                }
+            }
+        }
+        Split u[2][VT];
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int v = 0; v < VT; ++v) u[st][v] = split8(U[2 * st][v], U[2 * st + 1][v]);
+#pragma unroll
+        for (int t = 0; t < 8; ++t) {
+            const f32x4 d = *reinterpret_cast<const f32x4 *>(
+                ws + kWsD + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
+#pragma unroll
+            for (int v = 0; v < VT; ++v) S[t][v] *= d;
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                const char *kp = at + kWsK + (t * 2 + st) * 2048;
+                const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
+                const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
+#pragma unroll
+                for (int v = 0; v < VT; ++v) {
+                    S[t][v] = mfma(kh, u[st][v].hi, S[t][v]);
+                    S[t][v] = mfma(kh, u[st][v].lo, S[t][v]);
+                    S[t][v] = mfma(kl, u[st][v].hi, S[t][v]);
+                }
+            }
+        }
+#pragma unroll
+        for (int it = 0; it < 4; ++it) {
+#pragma unroll
+            for (int st = 0; st <= it >> 1; ++st) {
+                const u32x4 p = *reinterpret_cast<const u32x4 *>(at + kWsP + (it * 2 + st) * 1024);
+#pragma unroll
+                for (int v = 0; v < VT; ++v) {
+                    O[it][v] = mfma(u[st][v].hi, p, O[it][v]);
+                    O[it][v] = mfma(u[st][v].lo, p, O[it][v]);
+                }
+            }
+            if (it * 16 + lr < n) {
+                uint16_t *o = a.out + (size_t)(row0 + r0 + it * 16 + lr) * a.ldo + h * kHead +
+                              vt0 * 16 + lg * 4;
+#pragma unroll
+                for (int v = 0; v < VT; ++v)
+                    *reinterpret_cast<u32x2 *>(o + v * 16) = pack4(O[it][v]);
+            }
+        }
+    }
+#pragma unroll
+    for (int t = 0; t < 8; ++t)
+#pragma unroll
+        for (int v = 0; v < VT; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead + v * 16] =
+                    S[t][v][r];
+}
+
+// A launch holds the scan of one segment (its workgroups come first) and the
+// preparation of the next, which do not depend on each other.
+template <int VT, bool HEAD_GATE>
+__global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaSegment scan,
+                                                             DeltaSegment prep) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PARTS = 8 / VT / 4;  // workgroups a head in the scan
+    const int scans = scan.seqs * a.H * PARTS;
+    int i = blockIdx.x;
+    if (i < scans) {
+        const int part = i % PARTS;
+        const int h = i / PARTS % a.H;
+        const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
+        scan_columns<VT>(a, e[0], e[1], e[2], h, (part * 4 + scalar(threadIdx.x >> 6)) * VT,
+                         scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                         (size_t)a.H * kDeltaItemBytes);
+        return;
+    }
+    i -= scans;
+    const int h = i % a.H, c = i / a.H;
+    const int *e = prep.chunk_table + 2 * c;
+    prepare_item<HEAD_GATE>(a, e[0], e[1], h, prep.ws + (size_t)i * kDeltaItemBytes, lds);
+}
+
+template <int VT, bool HEAD_GATE>
+hipError_t launch(const DeltaArgs &a, const DeltaSegment &scan, const DeltaSegment &prep,
+                  hipStream_t st) {
+    const unsigned grid = (unsigned)(scan.seqs * a.H * (8 / VT / 4) + prep.chunks * a.H);
+    hipLaunchKernelGGL((delta_chunk_kernel<VT, HEAD_GATE>), dim3(grid), dim3(256),
+                       kDeltaPrepareLds, st, a, scan, prep);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
+                               const DeltaSegment &prep, bool head_gate, bool narrow,
+                               hipStream_t st) {
+    if (narrow)
+        return head_gate ? launch<1, true>(a, scan, prep, st) : launch<1, false>(a, scan, prep, st);
+    return head_gate ? launch<2, true>(a, scan, prep, st) : launch<2, false>(a, scan, prep, st);
+}
+
+hipError_t allow_delta_lds() {
+    hipError_t e = hipSuccess;
+    auto one = [&](const void *f) {
+        if (e == hipSuccess)
+            e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    kDeltaPrepareLds);
+    };
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, true>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, false>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, true>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, false>));
+    return e;
+}
+
+}  // namespace tp1
