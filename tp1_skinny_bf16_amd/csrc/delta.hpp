@@ -39,7 +39,7 @@ struct DeltaSeqs {
 // The chunked form.
 constexpr int kDeltaChunk = 64;             // tokens a chunk
 constexpr int kDeltaItemBytes = 123392;     // workspace of a chunk and head
-constexpr int kDeltaPrepareLds = 77056;     // LDS of a workgroup
+constexpr int kDeltaPrepareLds = 77072;     // LDS of a workgroup
 
 // A segment of the chunks: which to prepare, and which sequences to carry on.
 struct DeltaSegment {

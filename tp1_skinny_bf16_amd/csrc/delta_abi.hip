@@ -19,7 +19,8 @@ struct proj_delta_plan_s {
     int shorts = 0;              // sequences that run token by token
     std::vector<tp1::DeltaSegment> segments;
     void *mem = nullptr;         // device: tables, then two workspaces
-    const int *short_table = nullptr;
+    const int *seq_table = nullptr;    // all sequences
+    const int *short_table = nullptr;  // those that always run token by token
 };
 
 namespace tp1 {
@@ -89,11 +90,13 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
     for (int i = 0; i < n; ++i) {
         row[i] = r;
         r += lens[i];
+        t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
+    }
+    for (int i = 0; i < n; ++i)
         if (lens[i] > 0 && lens[i] <= kShortRows) {
             t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
             ++t.shorts;
         }
-    }
     const int per = (int)std::max(1L, kSegmentItems / H);
     struct Chunk {
         int seq, at;
@@ -177,7 +180,8 @@ int place(proj_delta_plan_s *p, Tables &t) {
         return PROJ_EHIP;
     const int *w = static_cast<const int *>(p->mem);
     p->shorts = t.shorts;
-    p->short_table = w;
+    p->seq_table = w;
+    p->short_table = w + 3 * (size_t)p->n;
     for (size_t i = 0; i < t.segments.size(); ++i) {
         t.segments[i].chunk_table = w + t.chunk_at[i];
         t.segments[i].seq_table = w + t.seq_at[i];
@@ -293,7 +297,11 @@ int proj_delta_run(const proj_delta_plan_t *p, const proj_delta_io_t *io, void *
     if (hipGetDevice(&cur) != hipSuccess || cur != p->device) return PROJ_EINVAL;
     const hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = hipSuccess;
-    if (p->shorts) {
+    if (!a.l2norm) {
+        const DeltaSeqs s{p->seq_table, nullptr, 0, p->n};
+        e = launch_delta_steps(a, s, io->head_gate, p->cus, st);
+        if (e == hipSuccess) return PROJ_OK;
+    } else if (p->shorts) {
         const DeltaSeqs s{p->short_table, nullptr, 0, p->shorts};
         e = launch_delta_steps(a, s, io->head_gate, p->cus, st);
     }

@@ -16,11 +16,18 @@
 //   scan (four waves a head, 32 columns of the state each, or eight of 16):
 //     chunk after chunk, U = U0 + W S, O = (Q e^G) S + P U, S' as above.
 //
-// Numbers.  All products run on the bf16 matrix cores with FP32 sums.  What
-// reaches the state (W, U, K, S as operands) is split into two bf16 values
-// hi + lo, and hi hi + hi lo + lo hi are summed: 2^-17 of each value is
-// lost, where one bf16 rounding would lose 2^-9 of the state a chunk.  What
-// only reaches the BF16 output (Q, P) is one bf16 value against a split one.
+// Numbers.  All products run on the 16-bit matrix cores with FP32 sums, and
+// what reaches the state is as exact as FP32 operands would make it.  Keys
+// and queries have unit length here (the chunked form is taken with l2norm
+// only), so every update is a contraction and T, W, K e^.. and Q e^.. stay
+// within 1: they are held as two FP16 values hi + lo of 2^10 times the value,
+// and hi hi + hi lo + lo hi summed, which drops 2^-23 of each (two BF16
+// values would drop 2^-17, one 2^-9).  S, U and V have any range: a wave
+// scales what it holds by a power of two that brings the largest magnitude
+// to 2^14.  What only reaches the BF16 output (Q, P, and the hi parts of S
+// and U against them) is one FP16 value each, 2^-12.  A and P are products
+// of decayed keys, whose range FP16 does not hold: BF16 in three parts with
+// the six largest products for A, in two parts with three for P.
 // Decays are products of factors e^x with x <= 0, the sums x taken inside
 // blocks of 16 tokens from the token outward, so none is a difference of
 // large numbers: with block a after block b, e^{G_i - G_j} = (e^{sum of a's
@@ -33,7 +40,7 @@
 //
 // Layout.  A wave of `prepare` owns one block of 16 tokens; lane l holds
 // token l % 16 and, for s = 0..3, channels 32 s + 8 (l / 16) + 0..7, which is
-// the A and B operand of v_mfma_f32_16x16x32_bf16 over channels.  Sums over
+// the A and B operand of v_mfma_f32_16x16x32 over channels.  Sums over
 // the tokens of a block are scans over 16 lanes (DPP).  Operands over tokens
 // need the transpose, which a product with a selection matrix gives exactly
 // (accumulator lane l holds rows 4 (l / 16) + 0..3 of column l % 16).  The
@@ -63,20 +70,30 @@ constexpr int kWsD = kWsU + 32768;            // [128] FP32
 static_assert(kWsD + 512 == kDeltaItemBytes, "workspace of an item");
 
 // LDS of `prepare`, in bytes.
-constexpr int kLdsKr = 0;                     // [hi, lo][48 rows][256], dead after barrier 2
+constexpr int kLdsKr = 0;                     // [48 rows][128] FP32, dead after barrier 2
 constexpr int kLdsT = 0;                      // [hi, lo][10 blocks][16 rows][40]
 constexpr int kLdsV = kLdsT + 2 * 10 * 640;   // [8 value tiles][2 steps][64][16]
 constexpr int kLdsK = kLdsV + 16384;          // [8 channel tiles][2 steps][hi, lo][64][16]
 constexpr int kLdsN = kLdsK + 32768;          // [10 blocks][16 rows][20] FP32
 constexpr int kLdsTot = kLdsN + 10 * 1280;    // [4][128] FP32
 constexpr int kLdsBeta = kLdsTot + 2048;      // [64] FP32
-static_assert(kLdsKr + 2 * 48 * 256 <= kLdsK, "the transposed values reuse the key rows");
-static_assert(kLdsBeta + 256 == kDeltaPrepareLds, "LDS of prepare");
+constexpr int kLdsTop = kLdsBeta + 256;       // [4] largest |v| of a block (bits)
+static_assert(kLdsKr + 48 * 512 <= kLdsK, "the transposed values reuse the key rows");
+static_assert(kLdsTop + 16 == kDeltaPrepareLds, "LDS of prepare");
 
-__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c) {
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+
+__device__ __forceinline__ f32x4 mfma_bf(u32x4 a, u32x4 b, f32x4 c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a),
                                                    __builtin_bit_cast(bf16x8_t, b), c, 0, 0, 0);
 }
+__device__ __forceinline__ f32x4 mfma_h(u32x4 a, u32x4 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a),
+                                                  __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
+}
+
+// What unit-bounded values are multiplied by before they become FP16 pairs.
+constexpr float kUnit = 1024.f;
 
 // e^x for x in [-8000, 88]: 2^(x log2 e) with the product's rounding error
 // put back to first order.
@@ -110,26 +127,62 @@ __device__ __forceinline__ float gate_of(float rate, float f, float bias) {
     return g < -120.f ? -120.f : g;
 }
 
+__device__ __forceinline__ unsigned pack_h(float a, float b) {
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(unsigned, f16x2_t{(_Float16)a, (_Float16)b});
+}
+__device__ __forceinline__ float h_lo(unsigned u) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)u);
+}
+__device__ __forceinline__ float h_hi(unsigned u) {
+    return (float)__builtin_bit_cast(_Float16, (uint16_t)(u >> 16));
+}
+
 struct Split {
     u32x4 hi, lo;
 };
-// Eight values as bf16 pairs hi + lo.
-__device__ __forceinline__ Split split8(const float *x) {
+// Eight values as FP16 pairs hi + lo; and one FP16 value each.
+__device__ __forceinline__ Split split_h(const float *x) {
     Split o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const unsigned h = pack_bf16(x[2 * i], x[2 * i + 1]);
+        const unsigned h = pack_h(x[2 * i], x[2 * i + 1]);
         o.hi[i] = h;
-        o.lo[i] = pack_bf16(x[2 * i] - bf16_lo(h), x[2 * i + 1] - bf16_hi(h));
+        o.lo[i] = pack_h(x[2 * i] - h_lo(h), x[2 * i + 1] - h_hi(h));
     }
     return o;
 }
-__device__ __forceinline__ Split split8(f32x4 a, f32x4 b) {
-    const float x[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
-    return split8(x);
+__device__ __forceinline__ u32x4 round_h(const float *x) {
+    return u32x4{pack_h(x[0], x[1]), pack_h(x[2], x[3]), pack_h(x[4], x[5]), pack_h(x[6], x[7])};
 }
-__device__ __forceinline__ u32x2 pack4(f32x4 a) {
-    return u32x2{pack_bf16(a.x, a.y), pack_bf16(a.z, a.w)};
+__device__ __forceinline__ Split split_h(f32x4 a, f32x4 b, float by) {
+    const float x[8] = {a.x * by, a.y * by, a.z * by, a.w * by,
+                        b.x * by, b.y * by, b.z * by, b.w * by};
+    return split_h(x);
+}
+__device__ __forceinline__ u32x2 pack4_h(f32x4 a) {
+    return u32x2{pack_h(a.x, a.y), pack_h(a.z, a.w)};
+}
+
+// Eight values as three BF16 parts, each the rounded rest of those before.
+struct Parts {
+    u32x4 p[3];
+};
+template <int N>
+__device__ __forceinline__ Parts split_bf(const float *x) {
+    Parts o;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float a = x[2 * i], b = x[2 * i + 1];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const unsigned h = pack_bf16(a, b);
+            o.p[k][i] = h;
+            a -= bf16_lo(h);
+            b -= bf16_hi(h);
+        }
+    }
+    return o;
 }
 __device__ __forceinline__ void unpack8(u32x4 v, float *x) {
 #pragma unroll
@@ -137,6 +190,28 @@ __device__ __forceinline__ void unpack8(u32x4 v, float *x) {
         x[2 * i] = bf16_lo(v[i]);
         x[2 * i + 1] = bf16_hi(v[i]);
     }
+}
+
+// A power of two that brings values of largest magnitude `top` (bits) to
+// 2^14..2^15, and its inverse.  Zeros, subnormals, infinities and NaN are
+// left as they are.
+struct Scale {
+    float up, down;
+};
+__device__ __forceinline__ Scale scale_for(unsigned top) {
+    const int e = (int)(top >> 23);  // biased exponent
+    int x = e == 0 || e == 255 ? 0 : 127 + 14 - e;
+    x = x > 120 ? 120 : x < -113 ? -113 : x;
+    return Scale{__uint_as_float((unsigned)(127 + x) << 23),
+                 __uint_as_float((unsigned)(127 - x) << 23)};
+}
+__device__ __forceinline__ unsigned top_of(f32x4 v, unsigned top) {
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const unsigned m = __float_as_uint(v[r]) & 0x7FFFFFFFu;
+        top = m > top ? m : top;
+    }
+    return top;
 }
 
 // Place of block (a, b), b <= a, among the lower triangle's ten.
@@ -196,8 +271,8 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 fv[s] = *reinterpret_cast<const u32x4 *>(a.f + row * a.ldf + h * kHead + c);
         }
     }
-    float rk = 1.f, rq = a.scale;
-    if (a.l2norm) {
+    float rk, rq;
+    {
         float sk = 0.f, sq = 0.f;
 #pragma unroll
         for (int s = 0; s < 4; ++s)
@@ -213,90 +288,108 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
         sk += __shfl_xor(sk, 32);
         sq += __shfl_xor(sq, 32);
         rk = rsqrtf(sk + kUnitEps);
-        rq *= rsqrtf(sq + kUnitEps);
+        rq = rsqrtf(sq + kUnitEps);
     }
     const float rate = expf(a.a_log[h]);
     if (lg == 0) betas[w * 16 + lr] = live ? sigmoid(bf16_value(a.b[row * a.ldb + h])) : 0.f;
 
-    float el[4][8], er[4][8], g[4][8];  // e^{sum up to}, e^{sum after}, log decay
+    float el[4][8], er[4][8];  // e^{sum up to}, e^{sum after}
     bool mild = true;
-    if constexpr (HEAD_GATE) {
-        const float gt = live ? gate_of(rate, bf16_value(a.f[row * a.ldf + h]), a.dt_bias[h]) : 0.f;
-        const float up = sum_upto(gt), after = sum_after(gt);
-        const float eu = exp_of(up), ea = exp_of(after);
-        mild = !(up < -40.f);
+    auto gates = [&](int s, float *g) {  // log decays of channels 32 s + 8 lg + 0..7
+        if constexpr (HEAD_GATE) {
+            const float x =
+                live ? gate_of(rate, bf16_value(a.f[row * a.ldf + h]), a.dt_bias[h]) : 0.f;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
+            for (int e = 0; e < 8; ++e) g[e] = x;
+        } else {
+            const f32x4 *bp =
+                reinterpret_cast<const f32x4 *>(a.dt_bias + h * kHead + 32 * s + 8 * lg);
+            const f32x4 b0 = bp[0], b1 = bp[1];
+            unpack8(fv[s], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[s][e] = gt, el[s][e] = eu, er[s][e] = ea;
-            if (lr == 15) {
-                f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + 32 * s + 8 * lg);
-                t[0] = t[1] = f32x4{up, up, up, up};
-            }
+            for (int e = 0; e < 8; ++e)
+                g[e] = live ? gate_of(rate, g[e], e < 4 ? b0[e & 3] : b1[e & 3]) : 0.f;
         }
-    } else {
+    };
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            const int c = 32 * s + 8 * lg;
-            float bias[8], up[8];
-            const f32x4 *bp = reinterpret_cast<const f32x4 *>(a.dt_bias + h * kHead + c);
-            *reinterpret_cast<f32x4 *>(bias) = bp[0];
-            *reinterpret_cast<f32x4 *>(bias + 4) = bp[1];
-            unpack8(fv[s], g[s]);
+    for (int s = 0; s < 4; ++s) {
+        const int c = 32 * s + 8 * lg;
+        float g[8], up[8];
+        if (!HEAD_GATE || s == 0) {
+            gates(s, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                g[s][e] = live ? gate_of(rate, g[s][e], bias[e]) : 0.f;
-                up[e] = sum_upto(g[s][e]);
+                if (HEAD_GATE && e > 0) {
+                    up[e] = up[0];
+                    el[s][e] = el[s][0];
+                    er[s][e] = er[s][0];
+                    continue;
+                }
+                up[e] = sum_upto(g[e]);
                 mild = mild && !(up[e] < -40.f);
                 el[s][e] = exp_of(up[e]);
-                er[s][e] = exp_of(sum_after(g[s][e]));
+                er[s][e] = exp_of(sum_after(g[e]));
             }
             if (lr == 15) {
                 f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + c);
                 t[0] = f32x4{up[0], up[1], up[2], up[3]};
                 t[1] = f32x4{up[4], up[5], up[6], up[7]};
+                if constexpr (HEAD_GATE) {
+#pragma unroll
+                    for (int o = 1; o < 4; ++o) t[8 * o] = t[8 * o + 1] = t[0];
+                }
             }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                el[s][e] = el[0][0];
+                er[s][e] = er[0][0];
+            }
+        }
+        // keys scaled to the end of their block, for the blocks after
+        if (w < 3) {
+            float x[8];
+            unpack8(kv[s], x);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= rk * er[s][e];
+            float *to = reinterpret_cast<float *>(lds + kLdsKr) + (w * 16 + lr) * 128;
+            const int p = (8 * s + 2 * lg) ^ (2 * lr);
+            *reinterpret_cast<f32x4 *>(to + p * 4) = f32x4{x[0], x[1], x[2], x[3]};
+            *reinterpret_cast<f32x4 *>(to + p * 4 + 4) = f32x4{x[4], x[5], x[6], x[7]};
         }
     }
     mild = __all(mild);
-
-    // ---- keys scaled to the end of their block, for the blocks after
-    float kf[4][8], qf[4][8];
-    Split kl[4];   // k e^{sum up to}
-    u32x4 ql[4];   // q e^{sum up to}, one bf16 value
-    float krf[4][8];
+    {
+        unsigned top = 0;
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-        unpack8(kv[s], kf[s]);
-        unpack8(qv[s], qf[s]);
-        float x[8], y[8];
+        for (int s = 0; s < 4; ++s)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            kf[s][e] *= rk;
-            qf[s][e] *= rq;
-            x[e] = kf[s][e] * el[s][e];
-            y[e] = qf[s][e] * el[s][e];
-            krf[s][e] = kf[s][e] * er[s][e];
-        }
-        kl[s] = split8(x);
-        ql[s] = split8(y).hi;
-        if (w < 3) {
-            const Split r = split8(krf[s]);
-            const int j = w * 16 + lr, p = (4 * s + lg) ^ lr;
-            *reinterpret_cast<u32x4 *>(lds + kLdsKr + j * 256 + p * 16) = r.hi;
-            *reinterpret_cast<u32x4 *>(lds + kLdsKr + 48 * 256 + j * 256 + p * 16) = r.lo;
-        }
+            for (int i = 0; i < 4; ++i) {
+                const unsigned lo = (vv[s][i] << 16) & 0x7FFFFFFFu, hi = vv[s][i] & 0x7FFF0000u;
+                top = lo > top ? lo : top;
+                top = hi > top ? hi : top;
+            }
+        top = max64(top);
+        if (lane == 0) reinterpret_cast<unsigned *>(lds + kLdsTop)[w] = top;
     }
-    __syncthreads();  // 1: key rows, block totals and betas are there
+    __syncthreads();  // 1: key rows, block totals, betas and the values' range are there
 
-    // ---- to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    f32x4 A[4], P[4];  // A[i = 4 lg + r][j = lr], P[j = 4 lg + r][i = lr] of blocks (w, 0..w)
+#pragma unroll
+    for (int b = 0; b < 4; ++b) A[b] = P[b] = none;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + 8 * lg;
-        float before[8], behind[8];
+        float kf[8], qf[8], before[8], behind[8];
+        unpack8(kv[s], kf);
+        unpack8(qv[s], qf);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) before[e] = behind[e] = 0.f;
+        for (int e = 0; e < 8; ++e) {
+            kf[e] *= rk;
+            qf[e] *= rq;
+            before[e] = behind[e] = 0.f;
+        }
 #pragma unroll
         for (int b = 0; b < 4; ++b) {
             const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c);
@@ -309,142 +402,187 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 behind[e + 4] += b > w ? t1[e] : 0.f;
             }
         }
-        float kt[8], kh[8], qt[8];
+        // to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
+        {
+            float kt[8], kh[8], qt[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                before[e] = exp_of(before[e]) * el[s][e];
+                kt[e] = kf[e] * before[e] * kUnit;
+                qt[e] = qf[e] * before[e] * kUnit;
+                kh[e] = kf[e] * er[s][e] * exp_of(behind[e]) * kUnit;
+            }
+            *reinterpret_cast<u32x4 *>(ws + kWsQ + ((w * 4 + s) * 64 + lane) * 16) = round_h(qt);
+            if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
+                f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
+                o[0] = f32x4{before[0], before[1], before[2], before[3]};
+                o[1] = f32x4{before[4], before[5], before[6], before[7]};
+            }
+            const Split st = split_h(kt), sh = split_h(kh);
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf) {
+                // column r of the selection picks channel 8 (r / 4) + 4 hf + r % 4
+                u32x4 sel = zero;
+                if (lg == lr >> 2) {
+                    const int e = (lr & 3) + 4 * hf;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        sel[i] = e >> 1 == i ? (e & 1 ? 0x3C000000u : 0x3C00u) : 0u;
+                }
+                const int at = ((2 * s + hf) * 2 + (w >> 1)) * 2048 + lane * 16 + (w & 1) * 8;
+                *reinterpret_cast<u32x2 *>(lds + kLdsK + at) = pack4_h(mfma_h(st.hi, sel, none));
+                *reinterpret_cast<u32x2 *>(lds + kLdsK + at + 1024) =
+                    pack4_h(mfma_h(st.lo, sel, none));
+                *reinterpret_cast<u32x2 *>(ws + kWsK + at) = pack4_h(mfma_h(sh.hi, sel, none));
+                *reinterpret_cast<u32x2 *>(ws + kWsK + at + 1024) =
+                    pack4_h(mfma_h(sh.lo, sel, none));
+            }
+        }
+        // A and P, block row w
+        float x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-            const float f = exp_of(before[e]);
-            kt[e] = kf[s][e] * el[s][e] * f;
-            qt[e] = qf[s][e] * el[s][e] * f;
-            kh[e] = krf[s][e] * exp_of(behind[e]);
+            x[e] = kf[e] * el[s][e];
+            y[e] = qf[e] * el[s][e];
         }
-        *reinterpret_cast<u32x4 *>(ws + kWsQ + ((w * 4 + s) * 64 + lane) * 16) = split8(qt).hi;
-        const Split st = split8(kt), sh = split8(kh);
-        if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
-            float d[8];
+        const Parts kl = split_bf<3>(x), ql = split_bf<2>(y);
+        auto add = [&](const float *right, f32x4 &Ab, f32x4 &Pb) {
+            const Parts r = split_bf<3>(right);
+            Ab = mfma_bf(kl.p[0], r.p[2], Ab);
+            Ab = mfma_bf(kl.p[2], r.p[0], Ab);
+            Ab = mfma_bf(kl.p[1], r.p[1], Ab);
+            Ab = mfma_bf(kl.p[0], r.p[1], Ab);
+            Ab = mfma_bf(kl.p[1], r.p[0], Ab);
+            Ab = mfma_bf(kl.p[0], r.p[0], Ab);
+            Pb = mfma_bf(r.p[1], ql.p[0], Pb);
+            Pb = mfma_bf(r.p[0], ql.p[1], Pb);
+            Pb = mfma_bf(r.p[0], ql.p[0], Pb);
+        };
+        if (mild) {
+            // e^{-(sum up to j)}; el is at least e^-40 here
 #pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = el[s][e] * exp_of(before[e]);
-            f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
-            o[0] = f32x4{d[0], d[1], d[2], d[3]};
-            o[1] = f32x4{d[4], d[5], d[6], d[7]};
+            for (int e = 0; e < 8; ++e) x[e] = kf[e] / el[s][e];
+            f32x4 Ad = none, Pd = none;
+            add(x, Ad, Pd);
+#pragma unroll
+            for (int b = 0; b < 4; ++b)
+                if (b == w) {
+                    A[b] += Ad;
+                    P[b] += Pd;
+                }
         }
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            // column r of the selection picks channel 8 (r / 4) + 4 hf + r % 4
-            u32x4 sel = zero;
-            if (lg == lr >> 2) {
-                const int e = (lr & 3) + 4 * hf;
+        for (int e = 0; e < 8; ++e) y[e] = 0.f;  // whole blocks between
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
+        for (int b = 2; b >= 0; --b) {
+            if (b >= w) continue;  // uniform
+            const float *from =
+                reinterpret_cast<const float *>(lds + kLdsKr) + (b * 16 + lr) * 128;
+            const int p = (8 * s + 2 * lg) ^ (2 * lr);
+            *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(from + p * 4);
+            *reinterpret_cast<f32x4 *>(x + 4) = *reinterpret_cast<const f32x4 *>(from + p * 4 + 4);
+            if (b < w - 1) {
+                const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tot + (b + 1) * kHead + c);
+                const f32x4 t1 = *reinterpret_cast<const f32x4 *>(tot + (b + 1) * kHead + c + 4);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    y[e] += e < 4 ? t0[e & 3] : t1[e & 3];
+                    x[e] *= exp_of(y[e]);
+                }
             }
-            const int at = ((2 * s + hf) * 2 + (w >> 1)) * 2048 + lane * 16 + (w & 1) * 8;
-            *reinterpret_cast<u32x2 *>(lds + kLdsK + at) = pack4(mfma(st.hi, sel, none));
-            *reinterpret_cast<u32x2 *>(lds + kLdsK + at + 1024) = pack4(mfma(st.lo, sel, none));
-            *reinterpret_cast<u32x2 *>(ws + kWsK + at) = pack4(mfma(sh.hi, sel, none));
-            *reinterpret_cast<u32x2 *>(ws + kWsK + at + 1024) = pack4(mfma(sh.lo, sel, none));
+            add(x, A[b], P[b]);
         }
     }
-
-    // ---- A (times beta, to LDS) and P (to the workspace), block row w
-    const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4);
-    for (int b = 0; b <= w; ++b) {
-        f32x4 A = none, P = none;  // A[i = 4 lg + r][j = lr], P[j = 4 lg + r][i = lr]
-        if (b < w || mild) {
+    if (!mild) {
+        // Exact inside a block: for d = 0..15, token i with j = i - d, the
+        // decay's exponent summed from i down.  Lane l holds i = l % 16.
+        float pi[16], ai[16];  // row i of P and A, by distance
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                Split r;
-                if (b == w) {
-                    float x[8];
+        for (int d = 0; d < 16; ++d) pi[d] = ai[d] = 0.f;
+#pragma unroll 1
+        for (int s = 0; s < 4; ++s) {
+            float gs[8], ks[8], kf[8], qf[8], x[8];
+            u32x4 kr = kv[0], qr = qv[0];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        // e^{-(sum up to j)}; el is at least e^-40 here
-                        x[e] = kf[s][e] / el[s][e];
+            for (int o = 1; o < 4; ++o) {
+                kr = s == o ? kv[o] : kr;
+                qr = s == o ? qv[o] : qr;
+            }
+            if constexpr (HEAD_GATE) {
+                gates(0, gs);
+            } else {
+                u32x4 fr = fv[0];
+#pragma unroll
+                for (int o = 1; o < 4; ++o) fr = s == o ? fv[o] : fr;
+                const float *bp = a.dt_bias + h * kHead + 32 * s + 8 * lg;
+                unpack8(fr, gs);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) gs[e] = live ? gate_of(rate, gs[e], bp[e]) : 0.f;
+            }
+            unpack8(kr, kf);
+            unpack8(qr, qf);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                kf[e] *= rk;
+                qf[e] *= rq;
+                ks[e] = kf[e];
+                x[e] = 0.f;
+            }
+#pragma unroll
+            for (int d = 0; d < 16; ++d)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    if (d > 0) {
+                        x[e] += gs[e];  // of token i - d + 1
+                        gs[e] = dpp_move<0x111>(gs[e]);
+                        ks[e] = dpp_move<0x111>(ks[e]);
                     }
-                    r = split8(x);
-                } else {
-                    const int p = (4 * s + lg) ^ lr;
-                    const char *at = lds + kLdsKr + (b * 16 + lr) * 256 + p * 16;
-                    r.hi = *reinterpret_cast<const u32x4 *>(at);
-                    r.lo = *reinterpret_cast<const u32x4 *>(at + 48 * 256);
-                    if (w - b > 1) {  // whole blocks between
-                        float x[8], y[8], m[8];
-                        unpack8(r.hi, x);
-                        unpack8(r.lo, y);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) m[e] = 0.f;
-                        for (int o = b + 1; o < w; ++o) {
-                            const float *t = tot + o * kHead + 32 * s + 8 * lg;
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) m[e] += t[e];
-                        }
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) x[e] = (x[e] + y[e]) * exp_of(m[e]);
-                        r = split8(x);
-                    }
+                    const float y = ks[e] * exp_of(x[e]);
+                    ai[d] = __builtin_fmaf(kf[e], y, ai[d]);
+                    pi[d] = __builtin_fmaf(qf[e], y, pi[d]);
                 }
-                A = mfma(kl[s].hi, r.hi, A);
-                A = mfma(kl[s].hi, r.lo, A);
-                A = mfma(kl[s].lo, r.hi, A);
-                P = mfma(r.hi, ql[s], P);
-                P = mfma(r.lo, ql[s], P);
-            }
-        } else {
-            // Exact inside a block: for d = 1..15, token i with j = i - d, the
-            // decay's exponent summed from i down.  Lane l holds i = l % 16.
-            float gs[4][8], ks[4][8], x[4][8];
-#pragma unroll
-            for (int s = 0; s < 4; ++s)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gs[s][e] = g[s][e], ks[s][e] = kf[s][e], x[s][e] = 0.f;
-            float *blk = Nb + block_of(w, w) * 320;
-            float pi[16], ai[16];  // row i of P and A, by distance
-#pragma unroll
-            for (int d = 0; d < 16; ++d) {
-                float pa = 0.f, pp = 0.f;
-#pragma unroll
-                for (int s = 0; s < 4; ++s)
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        if (d > 0) {
-                            x[s][e] += gs[s][e];  // of token i - d + 1
-                            gs[s][e] = dpp_move<0x111>(gs[s][e]);
-                            ks[s][e] = dpp_move<0x111>(ks[s][e]);
-                        }
-                        const float y = ks[s][e] * exp_of(x[s][e]);
-                        pa = __builtin_fmaf(kf[s][e], y, pa);
-                        pp = __builtin_fmaf(qf[s][e], y, pp);
-                    }
-                pa += __shfl_xor(pa, 16);
-                pp += __shfl_xor(pp, 16);
-                ai[d] = pa + __shfl_xor(pa, 32);
-                pi[d] = pp + __shfl_xor(pp, 32);
-            }
-            // through LDS (this wave's own block) into the accumulators' order
-#pragma unroll
-            for (int d = 0; d < 16; ++d)
-                if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = pi[d];
-            wave_sync();
-#pragma unroll
-            for (int r = 0; r < 4; ++r) P[r] = 4 * lg + r <= lr ? blk[lr * 20 + 4 * lg + r] : 0.f;
-            wave_sync();
-#pragma unroll
-            for (int d = 0; d < 16; ++d)
-                if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = ai[d];
-            wave_sync();
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                A[r] = lr <= 4 * lg + r ? blk[(4 * lg + r) * 20 + lr] : 0.f;
-            wave_sync();
         }
+        float *blk = Nb + block_of(w, w) * 320;  // this wave's own, free until below
+        f32x4 Ad, Pd;
+#pragma unroll
+        for (int d = 0; d < 16; ++d) {
+            ai[d] += __shfl_xor(ai[d], 16);
+            pi[d] += __shfl_xor(pi[d], 16);
+            ai[d] += __shfl_xor(ai[d], 32);
+            pi[d] += __shfl_xor(pi[d], 32);
+            if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = pi[d];
+        }
+        wave_sync();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Pd[r] = 4 * lg + r <= lr ? blk[lr * 20 + 4 * lg + r] : 0.f;
+        wave_sync();
+#pragma unroll
+        for (int d = 0; d < 16; ++d)
+            if (lg == 0 && d <= lr) blk[lr * 20 + lr - d] = ai[d];
+        wave_sync();
+#pragma unroll
+        for (int r = 0; r < 4; ++r) Ad[r] = lr <= 4 * lg + r ? blk[(4 * lg + r) * 20 + lr] : 0.f;
+        wave_sync();
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+            if (b == w) {
+                A[b] = Ad;
+                P[b] = Pd;
+            }
+    }
+    const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4);
+#pragma unroll
+    for (int b = 0; b < 4; ++b) {
+        if (b > w) continue;  // uniform
         float *blk = Nb + block_of(w, b) * 320;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (b == w && 4 * lg + r <= lr) A[r] = 0.f;  // strictly below the diagonal
-            if (b == w && 4 * lg + r > lr) P[r] = 0.f;   // on it and below
-            blk[(4 * lg + r) * 20 + lr] = A[r] * beta4[r];
+            if (b == w && 4 * lg + r <= lr) A[b][r] = 0.f;  // strictly below the diagonal
+            if (b == w && 4 * lg + r > lr) P[b][r] = 0.f;   // on it and below
+            blk[(4 * lg + r) * 20 + lr] = A[b][r] * beta4[r];
         }
         char *po = ws + kWsP + ((w * 2 + (b >> 1)) * 64 + lane) * 16;
-        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4(P);
+        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(P[b] * kUnit);
         if (b == w && (w & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
     }
     // ---- inverse of this block's 1 + N by forward substitution, a column a lane
@@ -466,7 +604,13 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
     }
     __syncthreads();  // 2: N below the diagonal and the inverses are there; key rows are free
 
-    // ---- V transposed, and column block w of the whole inverse
+    // ---- V transposed (scaled to FP16's range), and column block w of the whole inverse
+    Scale sv;
+    {
+        const u32x4 t = *reinterpret_cast<const u32x4 *>(lds + kLdsTop);
+        const unsigned x = t.x > t.y ? t.x : t.y, y = t.z > t.w ? t.z : t.w;
+        sv = scale_for(x > y ? x : y);
+    }
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -478,7 +622,8 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 for (int i = 0; i < 4; ++i)
                     sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
             *reinterpret_cast<u32x2 *>(lds + kLdsV + ((2 * s + hf) * 2 + (w >> 1)) * 1024 +
-                                       lane * 16 + (w & 1) * 8) = pack4(mfma(vv[s], sel, none));
+                                       lane * 16 + (w & 1) * 8) =
+                pack4_h(mfma_bf(vv[s], sel, none) * sv.up);
         }
     {
         const float bj = betas[w * 16 + lr];
@@ -487,11 +632,11 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             char *o = lds + kLdsT + block_of(ai, w) * 640 + lr * 2;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float x = t[r] * bj;
-                const uint16_t hi = round_bf16(x);
-                *reinterpret_cast<uint16_t *>(o + (4 * lg + r) * 40) = hi;
-                *reinterpret_cast<uint16_t *>(o + 6400 + (4 * lg + r) * 40) =
-                    round_bf16(x - bf16_value(hi));
+                const float x = t[r] * bj * kUnit;
+                const _Float16 hi = (_Float16)x;
+                *reinterpret_cast<_Float16 *>(o + (4 * lg + r) * 40) = hi;
+                *reinterpret_cast<_Float16 *>(o + 6400 + (4 * lg + r) * 40) =
+                    (_Float16)(x - (float)hi);
             }
         };
         const float *d = Nb + block_of(w, w) * 320;
@@ -553,21 +698,22 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 const u32x4 ko = *reinterpret_cast<const u32x4 *>(kp + 1024);
                 const u32x4 vt = *reinterpret_cast<const u32x4 *>(
                     lds + kLdsV + ((2 * w + hf) * 2 + st) * 1024 + lane * 16);
-                Wt[hf][it] = mfma(kh, th, Wt[hf][it]);
-                Wt[hf][it] = mfma(kh, tl, Wt[hf][it]);
-                Wt[hf][it] = mfma(ko, th, Wt[hf][it]);
-                U[it][hf] = mfma(th, vt, U[it][hf]);
-                U[it][hf] = mfma(tl, vt, U[it][hf]);
+                Wt[hf][it] = mfma_h(kh, tl, Wt[hf][it]);
+                Wt[hf][it] = mfma_h(ko, th, Wt[hf][it]);
+                Wt[hf][it] = mfma_h(kh, th, Wt[hf][it]);
+                U[it][hf] = mfma_h(tl, vt, U[it][hf]);
+                U[it][hf] = mfma_h(th, vt, U[it][hf]);
             }
         }
-        const Split o = split8(-Wt[0][it], -Wt[1][it]);
+        const Split o = split_h(Wt[0][it], Wt[1][it], -1.f / kUnit);
         char *wp = ws + kWsW + ((it * 4 + w) * 2 * 64 + lane) * 16;
         *reinterpret_cast<u32x4 *>(wp) = o.hi;
         *reinterpret_cast<u32x4 *>(wp + 1024) = o.lo;
+        const float back = sv.down / kUnit;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
             *reinterpret_cast<f32x4 *>(ws + kWsU + ((it * 8 + 2 * w + hf) * 64 + lane) * 16) =
-                U[it][hf];
+                U[it][hf] * back;
     }
 }
 
@@ -593,19 +739,25 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
     for (int r0 = 0; r0 < rows; r0 += kC, ws += ws_step) {
         const int n = min(kC, rows - r0);
         const char *at = ws + lane * 16;
-        f32x4 U[4][VT], O[4][VT];  // U[token][value], O[value][token] (transposed)
+        f32x4 U[4][VT];                    // [token][value]
+        f32x4 O[4][VT], OU[4][VT];         // [value][token]: Q S and P U
+        unsigned top = 0;
+#pragma unroll
+        for (int t = 0; t < 8; ++t)
+#pragma unroll
+            for (int v = 0; v < VT; ++v) top = top_of(S[t][v], top);
+        const Scale ss = scale_for(max64(top));
+        const float back = ss.down / kUnit;
 #pragma unroll
         for (int it = 0; it < 4; ++it)
 #pragma unroll
-            for (int v = 0; v < VT; ++v) {
-                U[it][v] = *reinterpret_cast<const f32x4 *>(at + kWsU + (it * 8 + vt0 + v) * 1024);
-                O[it][v] = f32x4{0.f, 0.f, 0.f, 0.f};
-            }
+            for (int v = 0; v < VT; ++v)
+                U[it][v] = O[it][v] = OU[it][v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int s = 0; s < 4; ++s) {
             Split b[VT];
 #pragma unroll
-            for (int v = 0; v < VT; ++v) b[v] = split8(S[2 * s][v], S[2 * s + 1][v]);
+            for (int v = 0; v < VT; ++v) b[v] = split_h(S[2 * s][v], S[2 * s + 1][v], ss.up);
 #pragma unroll
             for (int it = 0; it < 4; ++it) {
                 const char *wp = at + kWsW + (it * 4 + s) * 2048;
@@ -614,25 +766,38 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                 const u32x4 q = *reinterpret_cast<const u32x4 *>(at + kWsQ + (it * 4 + s) * 1024);
 #pragma unroll
                 for (int v = 0; v < VT; ++v) {
-                    U[it][v] = mfma(wh, b[v].hi, U[it][v]);
-                    U[it][v] = mfma(wh, b[v].lo, U[it][v]);
-                    U[it][v] = mfma(wl, b[v].hi, U[it][v]);
-                    O[it][v] = mfma(b[v].hi, q, O[it][v]);
-                    O[it][v] = mfma(b[v].lo, q, O[it][v]);
+                    U[it][v] = mfma_h(wh, b[v].lo, U[it][v]);
+                    U[it][v] = mfma_h(wl, b[v].hi, U[it][v]);
+                    U[it][v] = mfma_h(wh, b[v].hi, U[it][v]);
+                    O[it][v] = mfma_h(b[v].hi, q, O[it][v]);
                 }
             }
         }
+        top = 0;
+#pragma unroll
+        for (int it = 0; it < 4; ++it)
+#pragma unroll
+            for (int v = 0; v < VT; ++v) {
+                const f32x4 u0 =
+                    *reinterpret_cast<const f32x4 *>(at + kWsU + (it * 8 + vt0 + v) * 1024);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    U[it][v][r] = __builtin_fmaf(U[it][v][r], back, u0[r]);
+                top = top_of(U[it][v], top);
+            }
+        const Scale su = scale_for(max64(top));
         Split u[2][VT];
 #pragma unroll
         for (int st = 0; st < 2; ++st)
 #pragma unroll
-            for (int v = 0; v < VT; ++v) u[st][v] = split8(U[2 * st][v], U[2 * st + 1][v]);
+            for (int v = 0; v < VT; ++v)
+                u[st][v] = split_h(U[2 * st][v], U[2 * st + 1][v], su.up);
+        const float ub = su.down / kUnit;
 #pragma unroll
         for (int t = 0; t < 8; ++t) {
-            const f32x4 d = *reinterpret_cast<const f32x4 *>(
-                ws + kWsD + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
+            f32x4 x[VT];
 #pragma unroll
-            for (int v = 0; v < VT; ++v) S[t][v] *= d;
+            for (int v = 0; v < VT; ++v) x[v] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int st = 0; st < 2; ++st) {
                 const char *kp = at + kWsK + (t * 2 + st) * 2048;
@@ -640,29 +805,40 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                 const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
 #pragma unroll
                 for (int v = 0; v < VT; ++v) {
-                    S[t][v] = mfma(kh, u[st][v].hi, S[t][v]);
-                    S[t][v] = mfma(kh, u[st][v].lo, S[t][v]);
-                    S[t][v] = mfma(kl, u[st][v].hi, S[t][v]);
+                    x[v] = mfma_h(kh, u[st][v].lo, x[v]);
+                    x[v] = mfma_h(kl, u[st][v].hi, x[v]);
+                    x[v] = mfma_h(kh, u[st][v].hi, x[v]);
                 }
             }
+            const f32x4 d = *reinterpret_cast<const f32x4 *>(
+                ws + kWsD + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
+#pragma unroll
+            for (int v = 0; v < VT; ++v)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    S[t][v][r] = __builtin_fmaf(x[v][r], ub, S[t][v][r] * d[r]);
         }
+        const float os = back * a.scale, ou = ub * a.scale;
 #pragma unroll
         for (int it = 0; it < 4; ++it) {
 #pragma unroll
             for (int st = 0; st <= it >> 1; ++st) {
                 const u32x4 p = *reinterpret_cast<const u32x4 *>(at + kWsP + (it * 2 + st) * 1024);
 #pragma unroll
-                for (int v = 0; v < VT; ++v) {
-                    O[it][v] = mfma(u[st][v].hi, p, O[it][v]);
-                    O[it][v] = mfma(u[st][v].lo, p, O[it][v]);
-                }
+                for (int v = 0; v < VT; ++v) OU[it][v] = mfma_h(u[st][v].hi, p, OU[it][v]);
             }
             if (it * 16 + lr < n) {
                 uint16_t *o = a.out + (size_t)(row0 + r0 + it * 16 + lr) * a.ldo + h * kHead +
                               vt0 * 16 + lg * 4;
 #pragma unroll
-                for (int v = 0; v < VT; ++v)
-                    *reinterpret_cast<u32x2 *>(o + v * 16) = pack4(O[it][v]);
+                for (int v = 0; v < VT; ++v) {
+                    float x[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        x[r] = __builtin_fmaf(O[it][v][r], os, OU[it][v][r] * ou);
+                    *reinterpret_cast<u32x2 *>(o + v * 16) =
+                        u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+                }
             }
         }
     }
