@@ -7,6 +7,11 @@ values, times the state), and each inner product sums 128 terms (at most 140
 U32 of |S||k|).  With M the largest column norm of the states plus the
 largest |v|, a token adds at most 256 U32 * M, and n tokens 256 n U32 * M;
 outputs add that (|q| <= 1 after scaling) and half a BF16 step.
+The chunked form holds what reaches the state to 2^-23 of each value (and
+the output's operands to 2^-11 of their largest); errors of that kind are
+independent from element to element, so over the tokens a state remembers
+(about 64 of these gates) its relative error in the 2-norm is at most
+8 * 2^-23 = 2^-20.
 """
 import pytest
 import torch
@@ -42,6 +47,7 @@ def check(label, c, seqs, out, state, tokens, **kw):
         f"{do.max().item():.2e}")
     assert bool(torch.isfinite(state).all()) and bool(torch.isfinite(out.float()).all())
     assert ds.max().item() <= tol
+    assert rel <= 2.0 ** -20
     assert do.max().item() <= tol
     return want_o, want_s
 

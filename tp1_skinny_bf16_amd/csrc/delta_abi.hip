@@ -311,7 +311,7 @@ int proj_delta_run(const proj_delta_plan_t *p, const proj_delta_io_t *io, void *
         const DeltaSegment none{};
         const DeltaSegment &scan = i ? p->segments[i - 1] : none;
         const DeltaSegment &prep = i < n ? p->segments[i] : none;
-        e = launch_delta_chunks(a, scan, prep, io->head_gate, true, st);
+        e = launch_delta_chunks(a, scan, prep, io->head_gate, st);
     }
     if (e != hipSuccess) {
         (void)hipGetLastError();

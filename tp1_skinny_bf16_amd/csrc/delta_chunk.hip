@@ -13,8 +13,8 @@
 // in S is independent of the chunks before, so the work is in two parts:
 //   prepare (one workgroup a chunk and head): W = -T K e^G, U0 = T V, P,
 //     Q e^G, K e^{G_64 - G} and e^{G_64}, written to a workspace;
-//   scan (four waves a head, 32 columns of the state each, or eight of 16):
-//     chunk after chunk, U = U0 + W S, O = (Q e^G) S + P U, S' as above.
+//   scan (eight waves a head, 16 columns of the state each): chunk after chunk,
+//     U = U0 + W S, O = (Q e^G) S + P U, S' as above.
 //
 // Numbers.  All products run on the 16-bit matrix cores with FP32 sums, and
 // what reaches the state is as exact as FP32 operands would make it.  Keys
@@ -25,16 +25,15 @@
 // values would drop 2^-17, one 2^-9).  S, U and V have any range: a wave
 // scales what it holds by a power of two that brings the largest magnitude
 // to 2^14.  What only reaches the BF16 output (Q, P, and the hi parts of S
-// and U against them) is one FP16 value each, 2^-12.  A and P are products
-// of decayed keys, whose range FP16 does not hold: BF16 in three parts with
-// the six largest products for A, in two parts with three for P.
+// and U against them) is one FP16 value each, 2^-12.
 // Decays are products of factors e^x with x <= 0, the sums x taken inside
 // blocks of 16 tokens from the token outward, so none is a difference of
 // large numbers: with block a after block b, e^{G_i - G_j} = (e^{sum of a's
 // tokens up to i}) (e^{whole blocks between}) (e^{sum of b's tokens after
 // j}).  Inside a block the second factor is e^{-(sum up to j)} instead,
-// which grows: a block whose tokens decay a channel by more than e^-40 takes
-// an exact path on the vector unit (a running sum from i down to j).  A
+// which grows, so those products are FP32 ones (v_mfma_f32_16x16x4), and a
+// block whose tokens decay a channel by more than e^-40 takes an exact path
+// on the vector unit (a running sum from i down to j).  A
 // token's log decay is held above -120 (e^-120 is 0 in FP32), so that
 // infinite gates make no NaN.
 //
@@ -60,26 +59,39 @@ namespace {
 
 constexpr int kC = kDeltaChunk;   // tokens a chunk
 
-// Workspace of a chunk and head, in bytes.
-constexpr int kWsW = 0;                       // [4 token tiles][4 s][hi, lo][64][16]
-constexpr int kWsQ = kWsW + 32768;            // [4][4 s][64][16]
-constexpr int kWsK = kWsQ + 16384;            // [8 channel tiles][2 steps][hi, lo][64][16]
-constexpr int kWsP = kWsK + 32768;            // [4][2 steps][64][16]
-constexpr int kWsU = kWsP + 8192;             // [4][8 value tiles][64][16]
-constexpr int kWsD = kWsU + 32768;            // [128] FP32
-static_assert(kWsD + 512 == kDeltaItemBytes, "workspace of an item");
+// Workspace of a chunk and head: eight pieces of 12 KB, in the order the scan
+// takes them, then U0.  Everything in operand order, 16 bytes a lane:
+//   piece it = 0..3:      W of token tile it [4 s][hi, lo], Q e^G [4 s]
+//   piece 4 + s, s = 0..3: K e^{G_64 - G} of channel tiles 2 s, 2 s + 1 [2 steps]
+//                         [hi, lo], P of token tile s [2 steps], and (s = 0)
+//                         e^{G_64} [128] FP32
+//   U0:                   [4 token tiles][8 value tiles] FP32
+constexpr int kPiece = 12288;
+constexpr int kWsU = 8 * kPiece;
+static_assert(kWsU + 32768 == kDeltaItemBytes, "workspace of an item");
+constexpr int ws_w(int it, int s) { return it * kPiece + s * 2048; }
+constexpr int ws_q(int it, int s) { return it * kPiece + 8192 + s * 1024; }
+constexpr int ws_k(int tile, int step) {
+    return (4 + tile / 2) * kPiece + (tile % 2 * 2 + step) * 2048;
+}
+constexpr int ws_p(int it, int step) { return (4 + it) * kPiece + 8192 + step * 1024; }
+constexpr int kWsD = 4 * kPiece + 8192 + 2048;
 
 // LDS of `prepare`, in bytes.
-constexpr int kLdsKr = 0;                     // [48 rows][128] FP32, dead after barrier 2
+constexpr int kLdsKr = 0;                     // [48 rows][hi, lo][128] FP16, dead after barrier 2
 constexpr int kLdsT = 0;                      // [hi, lo][10 blocks][16 rows][40]
 constexpr int kLdsV = kLdsT + 2 * 10 * 640;   // [8 value tiles][2 steps][64][16]
 constexpr int kLdsK = kLdsV + 16384;          // [8 channel tiles][2 steps][hi, lo][64][16]
 constexpr int kLdsN = kLdsK + 32768;          // [10 blocks][16 rows][20] FP32
-constexpr int kLdsTot = kLdsN + 10 * 1280;    // [4][128] FP32
+constexpr int kLdsTot = kLdsN + 10 * 1280;    // [4][128] FP32: a block's whole decay
 constexpr int kLdsBeta = kLdsTot + 2048;      // [64] FP32
 constexpr int kLdsTop = kLdsBeta + 256;       // [4] largest |v| of a block (bits)
 static_assert(kLdsKr + 48 * 512 <= kLdsK, "the transposed values reuse the key rows");
-static_assert(kLdsTop + 16 == kDeltaPrepareLds, "LDS of prepare");
+static_assert(kLdsTop + 16 <= kDeltaLds, "LDS of prepare");
+// LDS of `scan`: a ring of piece slots, each with the wave's U0 tiles behind.
+constexpr int kSlots = 5;
+constexpr int kSlot = kPiece + 4096;
+static_assert(kSlots * kSlot <= kDeltaLds, "LDS of scan");
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
@@ -108,7 +120,9 @@ __device__ __forceinline__ float exp_of(float x) {
 // ln(1 + e^z) = max(z, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|z|; the
 // series in s^2 <= 1/9 stops below 2^-25 of the value.
 __device__ __forceinline__ float softplus_of(float z) {
-    const float e = exp_of(-fminf(fabsf(z), 200.f));
+    // an error of e scales the gate, whose own size it is weighed by: no
+    // correction of the exponent's rounding is needed here
+    const float e = __builtin_amdgcn_exp2f(-1.442695041f * fminf(fabsf(z), 200.f));
     const float s = e * __builtin_amdgcn_rcpf(2.f + e), t = s * s;
     float p = 1.f / 13.f;
     p = __builtin_fmaf(p, t, 1.f / 11.f);
@@ -138,6 +152,19 @@ __device__ __forceinline__ float h_hi(unsigned u) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)(u >> 16));
 }
 
+template <int I>
+struct Place {
+    static constexpr int value = I;
+};
+
+// The bits v as they are: without this the compiler may round a product to
+// FP16 twice, once fused with the product and once after its FP32 rounding,
+// and store one hi but subtract the other, a whole step apart.
+__device__ __forceinline__ unsigned settled(unsigned v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
 struct Split {
     u32x4 hi, lo;
 };
@@ -146,7 +173,7 @@ __device__ __forceinline__ Split split_h(const float *x) {
     Split o;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const unsigned h = pack_h(x[2 * i], x[2 * i + 1]);
+        const unsigned h = settled(pack_h(x[2 * i], x[2 * i + 1]));
         o.hi[i] = h;
         o.lo[i] = pack_h(x[2 * i] - h_lo(h), x[2 * i + 1] - h_hi(h));
     }
@@ -164,26 +191,6 @@ __device__ __forceinline__ u32x2 pack4_h(f32x4 a) {
     return u32x2{pack_h(a.x, a.y), pack_h(a.z, a.w)};
 }
 
-// Eight values as three BF16 parts, each the rounded rest of those before.
-struct Parts {
-    u32x4 p[3];
-};
-template <int N>
-__device__ __forceinline__ Parts split_bf(const float *x) {
-    Parts o;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        float a = x[2 * i], b = x[2 * i + 1];
-#pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const unsigned h = pack_bf16(a, b);
-            o.p[k][i] = h;
-            a -= bf16_lo(h);
-            b -= bf16_hi(h);
-        }
-    }
-    return o;
-}
 __device__ __forceinline__ void unpack8(u32x4 v, float *x) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -314,26 +321,25 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + 8 * lg;
-        float g[8], up[8];
+        float g[8];
         if (!HEAD_GATE || s == 0) {
             gates(s, g);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 if (HEAD_GATE && e > 0) {
-                    up[e] = up[0];
                     el[s][e] = el[s][0];
                     er[s][e] = er[s][0];
                     continue;
                 }
-                up[e] = sum_upto(g[e]);
-                mild = mild && !(up[e] < -40.f);
-                el[s][e] = exp_of(up[e]);
+                const float up = sum_upto(g[e]);
+                mild = mild && !(up < -40.f);
+                el[s][e] = exp_of(up);
                 er[s][e] = exp_of(sum_after(g[e]));
             }
             if (lr == 15) {
                 f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + c);
-                t[0] = f32x4{up[0], up[1], up[2], up[3]};
-                t[1] = f32x4{up[4], up[5], up[6], up[7]};
+                t[0] = f32x4{el[s][0], el[s][1], el[s][2], el[s][3]};
+                t[1] = f32x4{el[s][4], el[s][5], el[s][6], el[s][7]};
                 if constexpr (HEAD_GATE) {
 #pragma unroll
                     for (int o = 1; o < 4; ++o) t[8 * o] = t[8 * o + 1] = t[0];
@@ -351,11 +357,11 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             float x[8];
             unpack8(kv[s], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= rk * er[s][e];
-            float *to = reinterpret_cast<float *>(lds + kLdsKr) + (w * 16 + lr) * 128;
-            const int p = (8 * s + 2 * lg) ^ (2 * lr);
-            *reinterpret_cast<f32x4 *>(to + p * 4) = f32x4{x[0], x[1], x[2], x[3]};
-            *reinterpret_cast<f32x4 *>(to + p * 4 + 4) = f32x4{x[4], x[5], x[6], x[7]};
+            for (int e = 0; e < 8; ++e) x[e] *= rk * er[s][e] * kUnit;
+            const Split r = split_h(x);
+            char *to = lds + kLdsKr + (w * 16 + lr) * 512 + (((4 * s + lg) ^ lr) * 16);
+            *reinterpret_cast<u32x4 *>(to) = r.hi;
+            *reinterpret_cast<u32x4 *>(to + 256) = r.lo;
         }
     }
     mild = __all(mild);
@@ -375,48 +381,54 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
     __syncthreads();  // 1: key rows, block totals, betas and the values' range are there
 
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
-    f32x4 A[4], P[4];  // A[i = 4 lg + r][j = lr], P[j = 4 lg + r][i = lr] of blocks (w, 0..w)
+    // A[i = 4 lg + r][j = lr] and P[j = 4 lg + r][i = lr] of blocks (w, b < w) and (w, w)
+    f32x4 A[3], P[3], Ad = none, Pd = none;
 #pragma unroll
-    for (int b = 0; b < 4; ++b) A[b] = P[b] = none;
+    for (int b = 0; b < 3; ++b) A[b] = P[b] = none;
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + 8 * lg;
-        float kf[8], qf[8], before[8], behind[8];
+        float kf[8], qf[8];
         unpack8(kv[s], kf);
         unpack8(qv[s], qf);
+        // whole decays of the blocks before and behind this one
+        f32x4 t[4][2], before[2], behind[2];
+#pragma unroll
+        for (int b = 0; b < 4; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                t[b][i] = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c + 4 * i);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            before[i] = behind[i] = f32x4{1.f, 1.f, 1.f, 1.f};
+#pragma unroll
+            for (int b = 0; b < 3; ++b)
+                if (b < w) before[i] *= t[b][i];
+#pragma unroll
+            for (int b = 3; b > 0; --b)
+                if (b > w) behind[i] *= t[b][i];
+        }
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             kf[e] *= rk;
             qf[e] *= rq;
-            before[e] = behind[e] = 0.f;
-        }
-#pragma unroll
-        for (int b = 0; b < 4; ++b) {
-            const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c);
-            const f32x4 t1 = *reinterpret_cast<const f32x4 *>(tot + b * kHead + c + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                before[e] += b < w ? t0[e] : 0.f;
-                before[e + 4] += b < w ? t1[e] : 0.f;
-                behind[e] += b > w ? t0[e] : 0.f;
-                behind[e + 4] += b > w ? t1[e] : 0.f;
-            }
         }
         // to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
         {
-            float kt[8], kh[8], qt[8];
+            float kt[8], kh[8], qt[8], d[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                before[e] = exp_of(before[e]) * el[s][e];
-                kt[e] = kf[e] * before[e] * kUnit;
-                qt[e] = qf[e] * before[e] * kUnit;
-                kh[e] = kf[e] * er[s][e] * exp_of(behind[e]) * kUnit;
+                d[e] = before[e / 4][e % 4] * el[s][e];
+                const float x = d[e] * kUnit;
+                kt[e] = kf[e] * x;
+                qt[e] = qf[e] * x;
+                kh[e] = kf[e] * (er[s][e] * behind[e / 4][e % 4] * kUnit);
             }
-            *reinterpret_cast<u32x4 *>(ws + kWsQ + ((w * 4 + s) * 64 + lane) * 16) = round_h(qt);
+            *reinterpret_cast<u32x4 *>(ws + ws_q(0, s) + w * kPiece + lane * 16) = round_h(qt);
             if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
                 f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
-                o[0] = f32x4{before[0], before[1], before[2], before[3]};
-                o[1] = f32x4{before[4], before[5], before[6], before[7]};
+                o[0] = f32x4{d[0], d[1], d[2], d[3]};
+                o[1] = f32x4{d[4], d[5], d[6], d[7]};
             }
             const Split st = split_h(kt), sh = split_h(kh);
 #pragma unroll
@@ -429,69 +441,61 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                     for (int i = 0; i < 4; ++i)
                         sel[i] = e >> 1 == i ? (e & 1 ? 0x3C000000u : 0x3C00u) : 0u;
                 }
-                const int at = ((2 * s + hf) * 2 + (w >> 1)) * 2048 + lane * 16 + (w & 1) * 8;
-                *reinterpret_cast<u32x2 *>(lds + kLdsK + at) = pack4_h(mfma_h(st.hi, sel, none));
-                *reinterpret_cast<u32x2 *>(lds + kLdsK + at + 1024) =
-                    pack4_h(mfma_h(st.lo, sel, none));
-                *reinterpret_cast<u32x2 *>(ws + kWsK + at) = pack4_h(mfma_h(sh.hi, sel, none));
-                *reinterpret_cast<u32x2 *>(ws + kWsK + at + 1024) =
-                    pack4_h(mfma_h(sh.lo, sel, none));
+                const int half = lane * 16 + (w & 1) * 8;
+                char *kl = lds + kLdsK + ((2 * s + hf) * 2 + (w >> 1)) * 2048 + half;
+                char *kg = ws + ws_k(2 * s + hf, 0) + (w >> 1) * 2048 + half;
+                *reinterpret_cast<u32x2 *>(kl) = pack4_h(mfma_h(st.hi, sel, none));
+                *reinterpret_cast<u32x2 *>(kl + 1024) = pack4_h(mfma_h(st.lo, sel, none));
+                *reinterpret_cast<u32x2 *>(kg) = pack4_h(mfma_h(sh.hi, sel, none));
+                *reinterpret_cast<u32x2 *>(kg + 1024) = pack4_h(mfma_h(sh.lo, sel, none));
             }
         }
-        // A and P, block row w
+        // A and P, block row w: inside the block, then the blocks before
         float x[8], y[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             x[e] = kf[e] * el[s][e];
             y[e] = qf[e] * el[s][e];
         }
-        const Parts kl = split_bf<3>(x), ql = split_bf<2>(y);
-        auto add = [&](const float *right, f32x4 &Ab, f32x4 &Pb) {
-            const Parts r = split_bf<3>(right);
-            Ab = mfma_bf(kl.p[0], r.p[2], Ab);
-            Ab = mfma_bf(kl.p[2], r.p[0], Ab);
-            Ab = mfma_bf(kl.p[1], r.p[1], Ab);
-            Ab = mfma_bf(kl.p[0], r.p[1], Ab);
-            Ab = mfma_bf(kl.p[1], r.p[0], Ab);
-            Ab = mfma_bf(kl.p[0], r.p[0], Ab);
-            Pb = mfma_bf(r.p[1], ql.p[0], Pb);
-            Pb = mfma_bf(r.p[0], ql.p[1], Pb);
-            Pb = mfma_bf(r.p[0], ql.p[0], Pb);
-        };
         if (mild) {
-            // e^{-(sum up to j)}; el is at least e^-40 here
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = kf[e] / el[s][e];
-            f32x4 Ad = none, Pd = none;
-            add(x, Ad, Pd);
-#pragma unroll
-            for (int b = 0; b < 4; ++b)
-                if (b == w) {
-                    A[b] += Ad;
-                    P[b] += Pd;
-                }
+            for (int e = 0; e < 8; ++e) {
+                // e^{-(sum up to j)}; el is at least e^-40 here
+                const float r = kf[e] * __builtin_amdgcn_rcpf(el[s][e]);
+                Ad = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], r, Ad, 0, 0, 0);
+                Pd = __builtin_amdgcn_mfma_f32_16x16x4f32(r, y[e], Pd, 0, 0, 0);
+            }
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = 0.f;  // whole blocks between
+        for (int e = 0; e < 8; ++e) {
+            x[e] *= kUnit;
+            y[e] *= kUnit;
+        }
 #pragma unroll
         for (int b = 2; b >= 0; --b) {
             if (b >= w) continue;  // uniform
-            const float *from =
-                reinterpret_cast<const float *>(lds + kLdsKr) + (b * 16 + lr) * 128;
-            const int p = (8 * s + 2 * lg) ^ (2 * lr);
-            *reinterpret_cast<f32x4 *>(x) = *reinterpret_cast<const f32x4 *>(from + p * 4);
-            *reinterpret_cast<f32x4 *>(x + 4) = *reinterpret_cast<const f32x4 *>(from + p * 4 + 4);
-            if (b < w - 1) {
-                const f32x4 t0 = *reinterpret_cast<const f32x4 *>(tot + (b + 1) * kHead + c);
-                const f32x4 t1 = *reinterpret_cast<const f32x4 *>(tot + (b + 1) * kHead + c + 4);
+            if (b < w - 1) {       // through block b + 1
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
-                    y[e] += e < 4 ? t0[e & 3] : t1[e & 3];
-                    x[e] *= exp_of(y[e]);
+                    x[e] *= t[b + 1][e / 4][e % 4];
+                    y[e] *= t[b + 1][e / 4][e % 4];
                 }
             }
-            add(x, A[b], P[b]);
+            const Split l = split_h(x);
+            const u32x4 q = round_h(y);
+            const char *from = lds + kLdsKr + (b * 16 + lr) * 512 + (((4 * s + lg) ^ lr) * 16);
+            const u32x4 rh = *reinterpret_cast<const u32x4 *>(from);
+            const u32x4 rl = *reinterpret_cast<const u32x4 *>(from + 256);
+            A[b] = mfma_h(l.hi, rl, A[b]);
+            P[b] = mfma_h(rh, q, P[b]);
+            A[b] = mfma_h(l.lo, rh, A[b]);
+            A[b] = mfma_h(l.hi, rh, A[b]);
         }
+    }
+#pragma unroll
+    for (int b = 0; b < 3; ++b) {
+        A[b] *= 1.f / (kUnit * kUnit);
+        P[b] *= 1.f / (kUnit * kUnit);
     }
     if (!mild) {
         // Exact inside a block: for d = 0..15, token i with j = i - d, the
@@ -543,7 +547,6 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 }
         }
         float *blk = Nb + block_of(w, w) * 320;  // this wave's own, free until below
-        f32x4 Ad, Pd;
 #pragma unroll
         for (int d = 0; d < 16; ++d) {
             ai[d] += __shfl_xor(ai[d], 16);
@@ -563,27 +566,26 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
         for (int r = 0; r < 4; ++r) Ad[r] = lr <= 4 * lg + r ? blk[(4 * lg + r) * 20 + lr] : 0.f;
         wave_sync();
-#pragma unroll
-        for (int b = 0; b < 4; ++b)
-            if (b == w) {
-                A[b] = Ad;
-                P[b] = Pd;
-            }
     }
     const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4);
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         if (b > w) continue;  // uniform
+        f32x4 Ab = Ad, Pb = Pd;
+        if (b < 3 && b < w) {
+            Ab = A[b < 3 ? b : 0];
+            Pb = P[b < 3 ? b : 0];
+        }
         float *blk = Nb + block_of(w, b) * 320;
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            if (b == w && 4 * lg + r <= lr) A[b][r] = 0.f;  // strictly below the diagonal
-            if (b == w && 4 * lg + r > lr) P[b][r] = 0.f;   // on it and below
-            blk[(4 * lg + r) * 20 + lr] = A[b][r] * beta4[r];
+            if (b == w && 4 * lg + r <= lr) Ab[r] = 0.f;  // strictly below the diagonal
+            if (b == w && 4 * lg + r > lr) Pb[r] = 0.f;   // on it and below
+            blk[(4 * lg + r) * 20 + lr] = Ab[r] * beta4[r];
         }
-        char *po = ws + kWsP + ((w * 2 + (b >> 1)) * 64 + lane) * 16;
-        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(P[b] * kUnit);
-        if (b == w && (w & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
+        char *po = ws + ws_p(0, b >> 1) + w * kPiece + lane * 16;
+        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(Pb * kUnit);
+        if (b == w && (b & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
     }
     // ---- inverse of this block's 1 + N by forward substitution, a column a lane
     {
@@ -633,10 +635,10 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
                 const float x = t[r] * bj * kUnit;
-                const _Float16 hi = (_Float16)x;
-                *reinterpret_cast<_Float16 *>(o + (4 * lg + r) * 40) = hi;
+                const unsigned hi = settled(pack_h(x, 0.f));
+                *reinterpret_cast<uint16_t *>(o + (4 * lg + r) * 40) = (uint16_t)hi;
                 *reinterpret_cast<_Float16 *>(o + 6400 + (4 * lg + r) * 40) =
-                    (_Float16)(x - (float)hi);
+                    (_Float16)(x - h_lo(hi));
             }
         };
         const float *d = Nb + block_of(w, w) * 320;
@@ -706,7 +708,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             }
         }
         const Split o = split_h(Wt[0][it], Wt[1][it], -1.f / kUnit);
-        char *wp = ws + kWsW + ((it * 4 + w) * 2 * 64 + lane) * 16;
+        char *wp = ws + ws_w(it, 0) + w * 2048 + lane * 16;
         *reinterpret_cast<u32x4 *>(wp) = o.hi;
         *reinterpret_cast<u32x4 *>(wp + 1024) = o.lo;
         const float back = sv.down / kUnit;
@@ -718,156 +720,198 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 }
 
 // ---------------------------------------------------------------------------
-// scan: one wave a head and VT * 16 columns of its state, chunk after chunk.
+// scan: a workgroup of four waves a head and 64 columns of its state, 16
+// columns a wave, chunk after chunk.  A chunk's eight pieces go straight into
+// a ring of LDS slots (global_load_lds_dwordx4), kSlots - 1 pieces ahead,
+// and every wave reads its operands from there, so the state, which the next
+// chunk waits for, never waits for memory.  One barrier a piece.
 // ---------------------------------------------------------------------------
-template <int VT>
-__device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot,
-                                             int h, int vt0, const char *ws, size_t ws_step) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
+// 16 bytes a lane from src into LDS at base + 16 * lane (base uniform).  M0
+// needs one wait state between its write and the load that reads it.
+__device__ __forceinline__ void lds_load16(const void *src, uint32_t base) {
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
+                 :
+                 : "v"(src), "s"(base)
+                 : "memory", "m0");
+}
+#pragma clang diagnostic pop
+
+// A wave's loads of piece p: a quarter of the piece, and with W its own
+// columns of U0.
+constexpr int piece_loads(int p) { return p % 8 < 4 ? 4 : 3; }
+// Loads of the kSlots - 2 pieces after piece p, which may be in flight when
+// piece p is needed.
+constexpr int loads_after(int p) {
+    int n = 0;
+    for (int i = 1; i <= kSlots - 2; ++i) n += piece_loads(p + i);
+    return n;
+}
+
+__device__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot, int h, int part,
+                             const char *ws, size_t ws_step, char *lds) {
     const int lane = threadIdx.x & 63;
+    const int w = scalar(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) + vt0 * 16 + lr;
-    f32x4 S[8][VT];
+    const int vt = part * 4 + w;  // this wave's value tile
+    const int chunks = (rows + kC - 1) / kC;
+    const uint32_t lds0 =
+        scalar((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)lds);
+    float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) + vt * 16 + lr;
+    f32x4 S[8];
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int v = 0; v < VT; ++v)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                S[t][v][r] =
-                    state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead + v * 16];
+        for (int r = 0; r < 4; ++r)
+            S[t][r] = state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead];
+    wait_loads<0>();  // the ring's loads are counted from here
 
-    for (int r0 = 0; r0 < rows; r0 += kC, ws += ws_step) {
+    // the next piece to load: its place in the chunk is known where it is issued
+    int slot_in = 0, chunk_in = 0;
+    const char *ws_in = ws;
+    auto issue = [&](int p) {  // p: place of the piece in its chunk
+        const uint32_t to = lds0 + (uint32_t)(slot_in * kSlot);
+        const char *from = ws_in + p * kPiece + w * 3072 + lane * 16;
+#pragma unroll
+        for (int j = 0; j < 3; ++j)
+            lds_load16(from + j * 1024, to + (uint32_t)(w * 3072 + j * 1024));
+        if (p < 4)
+            lds_load16(ws_in + kWsU + (p * 8 + vt) * 1024 + lane * 16,
+                       to + (uint32_t)(kPiece + w * 1024));
+        slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
+        // past the last chunk the ring reads it again: nothing uses that
+        if (p == 7 && ++chunk_in < chunks) ws_in += ws_step;
+    };
+#pragma unroll
+    for (int p = 0; p < kSlots - 1; ++p) issue(p);
+
+    int slot_at = 0;
+    const char *in = lds;
+    auto next = [&](auto place) {  // piece `place` of the chunk has landed, the one before is free
+        constexpr int p = decltype(place)::value;
+        wait_loads<loads_after(p)>();
+        __syncthreads();
+        issue((p + kSlots - 1) % 8);
+        in = lds + slot_at * kSlot;
+        slot_at = slot_at + 1 == kSlots ? 0 : slot_at + 1;
+    };
+
+    const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    for (int r0 = 0; r0 < rows; r0 += kC) {
         const int n = min(kC, rows - r0);
-        const char *at = ws + lane * 16;
-        f32x4 U[4][VT];                    // [token][value]
-        f32x4 O[4][VT], OU[4][VT];         // [value][token]: Q S and P U
         unsigned top = 0;
 #pragma unroll
-        for (int t = 0; t < 8; ++t)
-#pragma unroll
-            for (int v = 0; v < VT; ++v) top = top_of(S[t][v], top);
+        for (int t = 0; t < 8; ++t) top = top_of(S[t], top);
         const Scale ss = scale_for(max64(top));
         const float back = ss.down / kUnit;
+        Split b[4];
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int v = 0; v < VT; ++v)
-                U[it][v] = O[it][v] = OU[it][v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            Split b[VT];
-#pragma unroll
-            for (int v = 0; v < VT; ++v) b[v] = split_h(S[2 * s][v], S[2 * s + 1][v], ss.up);
-#pragma unroll
-            for (int it = 0; it < 4; ++it) {
-                const char *wp = at + kWsW + (it * 4 + s) * 2048;
-                const u32x4 wh = *reinterpret_cast<const u32x4 *>(wp);
-                const u32x4 wl = *reinterpret_cast<const u32x4 *>(wp + 1024);
-                const u32x4 q = *reinterpret_cast<const u32x4 *>(at + kWsQ + (it * 4 + s) * 1024);
-#pragma unroll
-                for (int v = 0; v < VT; ++v) {
-                    U[it][v] = mfma_h(wh, b[v].lo, U[it][v]);
-                    U[it][v] = mfma_h(wl, b[v].hi, U[it][v]);
-                    U[it][v] = mfma_h(wh, b[v].hi, U[it][v]);
-                    O[it][v] = mfma_h(b[v].hi, q, O[it][v]);
-                }
-            }
-        }
+        for (int s = 0; s < 4; ++s) b[s] = split_h(S[2 * s], S[2 * s + 1], ss.up);
+        f32x4 U[4], O[4];  // U[token][value]; O[value][token] of Q S
         top = 0;
+        auto rows_of = [&](auto tile) {
+            constexpr int it = decltype(tile)::value;
+            next(tile);
+            const char *at = in + lane * 16;
+            f32x4 x = none, y = none, z = none, o = none;
 #pragma unroll
-        for (int it = 0; it < 4; ++it)
-#pragma unroll
-            for (int v = 0; v < VT; ++v) {
-                const f32x4 u0 =
-                    *reinterpret_cast<const f32x4 *>(at + kWsU + (it * 8 + vt0 + v) * 1024);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    U[it][v][r] = __builtin_fmaf(U[it][v][r], back, u0[r]);
-                top = top_of(U[it][v], top);
+            for (int s = 0; s < 4; ++s) {
+                const u32x4 wh = *reinterpret_cast<const u32x4 *>(at + s * 2048);
+                const u32x4 wl = *reinterpret_cast<const u32x4 *>(at + s * 2048 + 1024);
+                const u32x4 q = *reinterpret_cast<const u32x4 *>(at + 8192 + s * 1024);
+                x = mfma_h(wh, b[s].lo, x);
+                y = mfma_h(wl, b[s].hi, y);
+                z = mfma_h(wh, b[s].hi, z);
+                o = mfma_h(b[s].hi, q, o);
             }
+            O[it] = o;
+            const f32x4 u0 = *reinterpret_cast<const f32x4 *>(at + kPiece + w * 1024);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                U[it][r] = __builtin_fmaf((x[r] + y[r]) + z[r], back, u0[r]);
+            top = top_of(U[it], top);
+        };
+        rows_of(Place<0>{});
+        rows_of(Place<1>{});
+        rows_of(Place<2>{});
+        rows_of(Place<3>{});
         const Scale su = scale_for(max64(top));
-        Split u[2][VT];
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-            for (int v = 0; v < VT; ++v)
-                u[st][v] = split_h(U[2 * st][v], U[2 * st + 1][v], su.up);
         const float ub = su.down / kUnit;
+        const float os = back * a.scale, ou = ub * a.scale;
+        const Split u[2] = {split_h(U[0], U[1], su.up), split_h(U[2], U[3], su.up)};
+        auto channels_of = [&](auto quarter) {
+            constexpr int q = decltype(quarter)::value;
+            next(Place<4 + q>{});
+            const char *at = in + lane * 16;
+            if (q == 0) {
+                // the whole chunk's decays, of every piece's channels
 #pragma unroll
-        for (int t = 0; t < 8; ++t) {
-            f32x4 x[VT];
-#pragma unroll
-            for (int v = 0; v < VT; ++v) x[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                const char *kp = at + kWsK + (t * 2 + st) * 2048;
-                const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
-                const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
-#pragma unroll
-                for (int v = 0; v < VT; ++v) {
-                    x[v] = mfma_h(kh, u[st][v].lo, x[v]);
-                    x[v] = mfma_h(kl, u[st][v].hi, x[v]);
-                    x[v] = mfma_h(kh, u[st][v].hi, x[v]);
+                for (int t = 0; t < 8; ++t) {
+                    const f32x4 d = *reinterpret_cast<const f32x4 *>(
+                        in + (kWsD - 4 * kPiece) + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
+                    S[t] *= d;
                 }
             }
-            const f32x4 d = *reinterpret_cast<const f32x4 *>(
-                ws + kWsD + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
+            f32x4 x[2] = {none, none}, y[2] = {none, none}, o = none;
 #pragma unroll
-            for (int v = 0; v < VT; ++v)
+            for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    const char *kp = at + (hf * 2 + st) * 2048;
+                    const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
+                    const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
+                    x[hf] = mfma_h(kh, u[st].lo, x[hf]);
+                    y[hf] = mfma_h(kh, u[st].hi, y[hf]);
+                    x[hf] = mfma_h(kl, u[st].hi, x[hf]);
+                }
+#pragma unroll
+            for (int st = 0; st <= q >> 1; ++st) {
+                const u32x4 p = *reinterpret_cast<const u32x4 *>(at + 8192 + st * 1024);
+                o = mfma_h(u[st].hi, p, o);
+            }
+#pragma unroll
+            for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[t][v][r] = __builtin_fmaf(x[v][r], ub, S[t][v][r] * d[r]);
-        }
-        const float os = back * a.scale, ou = ub * a.scale;
+                    S[2 * q + hf][r] =
+                        __builtin_fmaf(x[hf][r] + y[hf][r], ub, S[2 * q + hf][r]);
+            if (q * 16 + lr < n) {
+                float v[4];
 #pragma unroll
-        for (int it = 0; it < 4; ++it) {
-#pragma unroll
-            for (int st = 0; st <= it >> 1; ++st) {
-                const u32x4 p = *reinterpret_cast<const u32x4 *>(at + kWsP + (it * 2 + st) * 1024);
-#pragma unroll
-                for (int v = 0; v < VT; ++v) OU[it][v] = mfma_h(u[st][v].hi, p, OU[it][v]);
+                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(O[q][r], os, o[r] * ou);
+                *reinterpret_cast<u32x2 *>(a.out + (size_t)(row0 + r0 + q * 16 + lr) * a.ldo +
+                                           h * kHead + vt * 16 + lg * 4) =
+                    u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
             }
-            if (it * 16 + lr < n) {
-                uint16_t *o = a.out + (size_t)(row0 + r0 + it * 16 + lr) * a.ldo + h * kHead +
-                              vt0 * 16 + lg * 4;
-#pragma unroll
-                for (int v = 0; v < VT; ++v) {
-                    float x[4];
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        x[r] = __builtin_fmaf(O[it][v][r], os, OU[it][v][r] * ou);
-                    *reinterpret_cast<u32x2 *>(o + v * 16) =
-                        u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-                }
-            }
-        }
+        };
+        channels_of(Place<0>{});
+        channels_of(Place<1>{});
+        channels_of(Place<2>{});
+        channels_of(Place<3>{});
     }
+    wait_loads<0>();  // no wave leaves LDS writes in flight
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-        for (int v = 0; v < VT; ++v)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead + v * 16] =
-                    S[t][v][r];
+        for (int r = 0; r < 4; ++r)
+            state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead] = S[t][r];
 }
 
 // A launch holds the scan of one segment (its workgroups come first) and the
 // preparation of the next, which do not depend on each other.
-template <int VT, bool HEAD_GATE>
+template <bool HEAD_GATE>
 __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaSegment scan,
                                                              DeltaSegment prep) {
     extern __shared__ __align__(16) char lds[];
-    constexpr int PARTS = 8 / VT / 4;  // workgroups a head in the scan
-    const int scans = scan.seqs * a.H * PARTS;
+    const int scans = scan.seqs * a.H * 2;  // two workgroups of 64 columns a head
     int i = blockIdx.x;
     if (i < scans) {
-        const int part = i % PARTS;
-        const int h = i / PARTS % a.H;
-        const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
-        scan_columns<VT>(a, e[0], e[1], e[2], h, (part * 4 + scalar(threadIdx.x >> 6)) * VT,
-                         scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
-                         (size_t)a.H * kDeltaItemBytes);
+        const int h = (i >> 1) % a.H;
+        const int *e = scan.seq_table + 4 * ((i >> 1) / a.H);
+        scan_columns(a, e[0], e[1], e[2], h, i & 1,
+                     scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                     (size_t)a.H * kDeltaItemBytes, lds);
         return;
     }
     i -= scans;
@@ -876,37 +920,26 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaS
     prepare_item<HEAD_GATE>(a, e[0], e[1], h, prep.ws + (size_t)i * kDeltaItemBytes, lds);
 }
 
-template <int VT, bool HEAD_GATE>
-hipError_t launch(const DeltaArgs &a, const DeltaSegment &scan, const DeltaSegment &prep,
-                  hipStream_t st) {
-    const unsigned grid = (unsigned)(scan.seqs * a.H * (8 / VT / 4) + prep.chunks * a.H);
-    hipLaunchKernelGGL((delta_chunk_kernel<VT, HEAD_GATE>), dim3(grid), dim3(256),
-                       kDeltaPrepareLds, st, a, scan, prep);
-    return hipGetLastError();
-}
-
 }  // namespace
 
 hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
-                               const DeltaSegment &prep, bool head_gate, bool narrow,
-                               hipStream_t st) {
-    if (narrow)
-        return head_gate ? launch<1, true>(a, scan, prep, st) : launch<1, false>(a, scan, prep, st);
-    return head_gate ? launch<2, true>(a, scan, prep, st) : launch<2, false>(a, scan, prep, st);
+                               const DeltaSegment &prep, bool head_gate, hipStream_t st) {
+    const dim3 grid((unsigned)(scan.seqs * a.H * 2 + prep.chunks * a.H));
+    if (head_gate)
+        hipLaunchKernelGGL(delta_chunk_kernel<true>, grid, dim3(256), kDeltaLds, st, a, scan, prep);
+    else
+        hipLaunchKernelGGL(delta_chunk_kernel<false>, grid, dim3(256), kDeltaLds, st, a, scan,
+                           prep);
+    return hipGetLastError();
 }
 
 hipError_t allow_delta_lds() {
-    hipError_t e = hipSuccess;
-    auto one = [&](const void *f) {
-        if (e == hipSuccess)
-            e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize,
-                                    kDeltaPrepareLds);
-    };
-    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, true>));
-    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, false>));
-    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, true>));
-    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, false>));
-    return e;
+    const auto attr = hipFuncAttributeMaxDynamicSharedMemorySize;
+    const hipError_t e = hipFuncSetAttribute(
+        reinterpret_cast<const void *>(&delta_chunk_kernel<true>), attr, kDeltaLds);
+    if (e != hipSuccess) return e;
+    return hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_chunk_kernel<false>), attr,
+                               kDeltaLds);
 }
 
 }  // namespace tp1
