@@ -32,10 +32,8 @@
 // tokens up to i}) (e^{whole blocks between}) (e^{sum of b's tokens after
 // j}).  Inside a block the second factor is e^{-(sum up to j)} instead,
 // which grows, so those products are FP32 ones (v_mfma_f32_16x16x4), and a
-// block whose tokens decay a channel by more than e^-40 takes an exact path
-// on the vector unit (a running sum from i down to j).  A
-// token's log decay is held above -120 (e^-120 is 0 in FP32), so that
-// infinite gates make no NaN.
+// block whose tokens decay a channel by more than 2^-58 takes an exact path
+// on the vector unit (a running sum from i down to j).
 //
 // Layout.  A wave of `prepare` owns one block of 16 tokens; lane l holds
 // token l % 16 and, for s = 0..3, channels 32 s + 8 (l / 16) + 0..7, which is
@@ -104,41 +102,32 @@ __device__ __forceinline__ f32x4 mfma_h(u32x4 a, u32x4 b, f32x4 c) {
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
+// A block is mild if no channel decays by more than 2^-kMild over it.
+constexpr float kMild = 58.f;
+
 // What unit-bounded values are multiplied by before they become FP16 pairs.
 constexpr float kUnit = 1024.f;
 
-// e^x for x in [-8000, 88]: 2^(x log2 e) with the product's rounding error
-// put back to first order.
-__device__ __forceinline__ float exp_of(float x) {
-    const float t = x * 1.442695041f;
-    float r = __builtin_fmaf(x, 1.442695041f, -t);
-    r = __builtin_fmaf(x, 1.92596299e-8f, r);  // log2 e beyond its FP32 value
-    const float e = __builtin_amdgcn_exp2f(t);
-    return __builtin_fmaf(e, r * 0.6931472f, e);
-}
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
 
-// ln(1 + e^z) = max(z, 0) + 2 atanh(s), s = e / (2 + e), e = e^-|z|; the
-// series in s^2 <= 1/9 stops below 2^-25 of the value.
-__device__ __forceinline__ float softplus_of(float z) {
-    // an error of e scales the gate, whose own size it is weighed by: no
-    // correction of the exponent's rounding is needed here
-    const float e = __builtin_amdgcn_exp2f(-1.442695041f * fminf(fabsf(z), 200.f));
-    const float s = e * __builtin_amdgcn_rcpf(2.f + e), t = s * s;
-    float p = 1.f / 13.f;
-    p = __builtin_fmaf(p, t, 1.f / 11.f);
-    p = __builtin_fmaf(p, t, 1.f / 9.f);
-    p = __builtin_fmaf(p, t, 1.f / 7.f);
-    p = __builtin_fmaf(p, t, 1.f / 5.f);
-    p = __builtin_fmaf(p, t, 1.f / 3.f);
-    p = __builtin_fmaf(p, t, 1.f);
-    const float r = fmaxf(z, 0.f) + 2.f * s * p;
-    return z == z ? r : z;
-}
-
-// A token's log decay, held above -120.
+// log2 of a token's decay: -rate * ln(1 + e^z), z = f + dt_bias, where rate is
+// exp(A_log) log2 e.  ln(1 + e^z) = max(z, 0) + 2 atanh(s) with s = e / (2 +
+// e), e = e^-|z|; the series in s^2 <= 1/9 stops below 2^-25 of the value.
+// (The rounding of e's exponent is an error relative to the gate itself,
+// which weighs nothing where e is far from 1.)  Sums of gates stay in base
+// 2, where e^x costs one instruction; infinite ones end as factors 0.
 __device__ __forceinline__ float gate_of(float rate, float f, float bias) {
-    const float g = -rate * softplus_of(f + bias);
-    return g < -120.f ? -120.f : g;
+    const float z = f + bias;
+    const float e = exp2_of(-1.442695041f * fabsf(z));
+    const float s = e * __builtin_amdgcn_rcpf(2.f + e), t = s * s;
+    float p = 2.f / 13.f;
+    p = __builtin_fmaf(p, t, 2.f / 11.f);
+    p = __builtin_fmaf(p, t, 2.f / 9.f);
+    p = __builtin_fmaf(p, t, 2.f / 7.f);
+    p = __builtin_fmaf(p, t, 2.f / 5.f);
+    p = __builtin_fmaf(p, t, 2.f / 3.f);
+    p = __builtin_fmaf(p, t, 2.f);
+    return -rate * __builtin_fmaf(s, p, fmaxf(z, 0.f));
 }
 
 __device__ __forceinline__ unsigned pack_h(float a, float b) {
@@ -161,6 +150,11 @@ struct Place {
 // FP16 twice, once fused with the product and once after its FP32 rounding,
 // and store one hi but subtract the other, a whole step apart.
 __device__ __forceinline__ unsigned settled(unsigned v) {
+    asm("" : "+v"(v));
+    return v;
+}
+
+__device__ __forceinline__ float settled(float v) {
     asm("" : "+v"(v));
     return v;
 }
@@ -278,7 +272,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 fv[s] = *reinterpret_cast<const u32x4 *>(a.f + row * a.ldf + h * kHead + c);
         }
     }
-    float rk, rq;
+    float rk, rq;  // to 2^10 times unit length
     {
         float sk = 0.f, sq = 0.f;
 #pragma unroll
@@ -294,28 +288,30 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
         sq += __shfl_xor(sq, 16);
         sk += __shfl_xor(sk, 32);
         sq += __shfl_xor(sq, 32);
-        rk = rsqrtf(sk + kUnitEps);
-        rq = rsqrtf(sq + kUnitEps);
+        rk = rsqrtf(sk + kUnitEps) * kUnit;
+        rq = rsqrtf(sq + kUnitEps) * kUnit;
     }
-    const float rate = expf(a.a_log[h]);
+    const float rate = expf(a.a_log[h]) * 1.442695041f;
     if (lg == 0) betas[w * 16 + lr] = live ? sigmoid(bf16_value(a.b[row * a.ldb + h])) : 0.f;
 
-    float el[4][8], er[4][8];  // e^{sum up to}, e^{sum after}
-    bool mild = true;
-    auto gates = [&](int s, float *g) {  // log decays of channels 32 s + 8 lg + 0..7
+    float el[4][8], er[4][8];  // decay of the block's tokens up to and with this one; after it
+    float least = 0.f;
+    auto gates = [&](int s, float *g) {  // log2 decays of channels 32 s + 8 lg + 0..7
         if constexpr (HEAD_GATE) {
-            const float x =
-                live ? gate_of(rate, bf16_value(a.f[row * a.ldf + h]), a.dt_bias[h]) : 0.f;
+            const float x = gate_of(rate, live ? bf16_value(a.f[row * a.ldf + h]) : 0.f,
+                                    a.dt_bias[h]);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) g[e] = x;
+            for (int e = 0; e < 8; ++e) g[e] = live ? x : 0.f;
         } else {
             const f32x4 *bp =
                 reinterpret_cast<const f32x4 *>(a.dt_bias + h * kHead + 32 * s + 8 * lg);
             const f32x4 b0 = bp[0], b1 = bp[1];
             unpack8(fv[s], g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                g[e] = live ? gate_of(rate, g[e], e < 4 ? b0[e & 3] : b1[e & 3]) : 0.f;
+            for (int e = 0; e < 8; ++e) {
+                const float x = settled(gate_of(rate, g[e], e < 4 ? b0[e & 3] : b1[e & 3]));
+                g[e] = live ? x : 0.f;  // computed first: a branch a channel costs more
+            }
         }
     };
 #pragma unroll
@@ -332,9 +328,9 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                     continue;
                 }
                 const float up = sum_upto(g[e]);
-                mild = mild && !(up < -40.f);
-                el[s][e] = exp_of(up);
-                er[s][e] = exp_of(sum_after(g[e]));
+                least = fminf(least, up);
+                el[s][e] = exp2_of(up);
+                er[s][e] = exp2_of(sum_after(g[e]));
             }
             if (lr == 15) {
                 f32x4 *t = reinterpret_cast<f32x4 *>(tot + w * kHead + c);
@@ -357,14 +353,14 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             float x[8];
             unpack8(kv[s], x);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] *= rk * er[s][e] * kUnit;
+            for (int e = 0; e < 8; ++e) x[e] *= rk * er[s][e];
             const Split r = split_h(x);
             char *to = lds + kLdsKr + (w * 16 + lr) * 512 + (((4 * s + lg) ^ lr) * 16);
             *reinterpret_cast<u32x4 *>(to) = r.hi;
             *reinterpret_cast<u32x4 *>(to + 256) = r.lo;
         }
     }
-    mild = __all(mild);
+    const bool mild = __all(least > -kMild);
     {
         unsigned top = 0;
 #pragma unroll
@@ -381,6 +377,12 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
     __syncthreads();  // 1: key rows, block totals, betas and the values' range are there
 
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    unsigned pick0 = 0, pick1 = 0;  // FP16 one for channel lr % 4 of four, in its lane group
+    if (lg == lr >> 2) {
+        const unsigned one = lr & 1 ? 0x3C000000u : 0x3C00u;
+        pick0 = lr & 2 ? 0u : one;
+        pick1 = lr & 2 ? one : 0u;
+    }
     // A[i = 4 lg + r][j = lr] and P[j = 4 lg + r][i = lr] of blocks (w, b < w) and (w, w)
     f32x4 A[3], P[3], Ad = none, Pd = none;
 #pragma unroll
@@ -388,7 +390,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + 8 * lg;
-        float kf[8], qf[8];
+        float kf[8], qf[8], x[8], y[8];
         unpack8(kv[s], kf);
         unpack8(qv[s], qf);
         // whole decays of the blocks before and behind this one
@@ -411,36 +413,30 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
             kf[e] *= rk;
-            qf[e] *= rq;
+            x[e] = kf[e] * el[s][e];
+            y[e] = qf[e] * rq * el[s][e];
         }
         // to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
         {
-            float kt[8], kh[8], qt[8], d[8];
+            float kt[8], kh[8], qt[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                d[e] = before[e / 4][e % 4] * el[s][e];
-                const float x = d[e] * kUnit;
-                kt[e] = kf[e] * x;
-                qt[e] = qf[e] * x;
-                kh[e] = kf[e] * (er[s][e] * behind[e / 4][e % 4] * kUnit);
+                kt[e] = x[e] * before[e / 4][e % 4];
+                qt[e] = y[e] * before[e / 4][e % 4];
+                kh[e] = kf[e] * er[s][e] * behind[e / 4][e % 4];
             }
             *reinterpret_cast<u32x4 *>(ws + ws_q(0, s) + w * kPiece + lane * 16) = round_h(qt);
             if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
                 f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
-                o[0] = f32x4{d[0], d[1], d[2], d[3]};
-                o[1] = f32x4{d[4], d[5], d[6], d[7]};
+                o[0] = f32x4{el[s][0], el[s][1], el[s][2], el[s][3]} * before[0];
+                o[1] = f32x4{el[s][4], el[s][5], el[s][6], el[s][7]} * before[1];
             }
             const Split st = split_h(kt), sh = split_h(kh);
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 // column r of the selection picks channel 8 (r / 4) + 4 hf + r % 4
-                u32x4 sel = zero;
-                if (lg == lr >> 2) {
-                    const int e = (lr & 3) + 4 * hf;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        sel[i] = e >> 1 == i ? (e & 1 ? 0x3C000000u : 0x3C00u) : 0u;
-                }
+                const u32x4 sel =
+                    hf ? u32x4{0u, 0u, pick0, pick1} : u32x4{pick0, pick1, 0u, 0u};
                 const int half = lane * 16 + (w & 1) * 8;
                 char *kl = lds + kLdsK + ((2 * s + hf) * 2 + (w >> 1)) * 2048 + half;
                 char *kg = ws + ws_k(2 * s + hf, 0) + (w >> 1) * 2048 + half;
@@ -451,25 +447,14 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             }
         }
         // A and P, block row w: inside the block, then the blocks before
-        float x[8], y[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] = kf[e] * el[s][e];
-            y[e] = qf[e] * el[s][e];
-        }
         if (mild) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // e^{-(sum up to j)}; el is at least e^-40 here
+                // e^{-(sum up to j)}; el is at least 2^-58 here
                 const float r = kf[e] * __builtin_amdgcn_rcpf(el[s][e]);
                 Ad = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], r, Ad, 0, 0, 0);
                 Pd = __builtin_amdgcn_mfma_f32_16x16x4f32(r, y[e], Pd, 0, 0, 0);
             }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            x[e] *= kUnit;
-            y[e] *= kUnit;
         }
 #pragma unroll
         for (int b = 2; b >= 0; --b) {
@@ -491,11 +476,6 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             A[b] = mfma_h(l.lo, rh, A[b]);
             A[b] = mfma_h(l.hi, rh, A[b]);
         }
-    }
-#pragma unroll
-    for (int b = 0; b < 3; ++b) {
-        A[b] *= 1.f / (kUnit * kUnit);
-        P[b] *= 1.f / (kUnit * kUnit);
     }
     if (!mild) {
         // Exact inside a block: for d = 0..15, token i with j = i - d, the
@@ -541,7 +521,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                         gs[e] = dpp_move<0x111>(gs[e]);
                         ks[e] = dpp_move<0x111>(ks[e]);
                     }
-                    const float y = ks[e] * exp_of(x[e]);
+                    const float y = ks[e] * exp2_of(x[e]);
                     ai[d] = __builtin_fmaf(kf[e], y, ai[d]);
                     pi[d] = __builtin_fmaf(qf[e], y, pi[d]);
                 }
@@ -567,7 +547,9 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
         for (int r = 0; r < 4; ++r) Ad[r] = lr <= 4 * lg + r ? blk[(4 * lg + r) * 20 + lr] : 0.f;
         wave_sync();
     }
-    const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4);
+    // A and P come as 2^20 times their values
+    const f32x4 beta4 = *reinterpret_cast<const f32x4 *>(betas + w * 16 + lg * 4) *
+                        (1.f / (kUnit * kUnit));
 #pragma unroll
     for (int b = 0; b < 4; ++b) {
         if (b > w) continue;  // uniform
@@ -584,7 +566,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             blk[(4 * lg + r) * 20 + lr] = Ab[r] * beta4[r];
         }
         char *po = ws + ws_p(0, b >> 1) + w * kPiece + lane * 16;
-        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(Pb * kUnit);
+        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(Pb * (1.f / kUnit));
         if (b == w && (b & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
     }
     // ---- inverse of this block's 1 + N by forward substitution, a column a lane
@@ -628,50 +610,39 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
                 pack4_h(mfma_bf(vv[s], sel, none) * sv.up);
         }
     {
-        const float bj = betas[w * 16 + lr];
-        f32x4 T[4];
+        const float bj = betas[w * 16 + lr] * kUnit;
         auto store_t = [&](int ai, f32x4 t) {  // T_ab diag(beta), rows i = 4 lg + r, column lr
             char *o = lds + kLdsT + block_of(ai, w) * 640 + lr * 2;
 #pragma unroll
             for (int r = 0; r < 4; ++r) {
-                const float x = t[r] * bj * kUnit;
+                const float x = t[r] * bj;
                 const unsigned hi = settled(pack_h(x, 0.f));
                 *reinterpret_cast<uint16_t *>(o + (4 * lg + r) * 40) = (uint16_t)hi;
                 *reinterpret_cast<_Float16 *>(o + 6400 + (4 * lg + r) * 40) =
                     (_Float16)(x - h_lo(hi));
             }
         };
+        auto times = [&](int ai, int bi, f32x4 t, f32x4 acc) {  // block (ai, bi) of N times t
+            const f32x4 nv =
+                *reinterpret_cast<const f32x4 *>(Nb + block_of(ai, bi) * 320 + lr * 20 + lg * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(nv[r], t[r], acc, 0, 0, 0);
+            return acc;
+        };
+        // T_ww is the block's inverse; T_aw = -(inverse of a) (sum_c N_ac T_cw)
         const float *d = Nb + block_of(w, w) * 320;
-        f32x4 t;
+        f32x4 t, X[4] = {none, none, none, none};
 #pragma unroll
         for (int r = 0; r < 4; ++r) t[r] = d[(4 * lg + r) * 20 + lr];
         store_t(w, t);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) T[i] = none;
+        for (int c = 0; c < 3; ++c) {
+            if (c < w) continue;  // uniform
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (i == w) T[i] = t;
-#pragma unroll
-        for (int i = 1; i < 4; ++i) {
-            if (i <= w) continue;  // uniform
-            f32x4 X = none;
-#pragma unroll
-            for (int c = 0; c < 3; ++c) {
-                if (c < w || c >= i) continue;
-                const f32x4 nv =
-                    *reinterpret_cast<const f32x4 *>(Nb + block_of(i, c) * 320 + lr * 20 + lg * 4);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    X = __builtin_amdgcn_mfma_f32_16x16x4f32(nv[r], T[c][r], X, 0, 0, 0);
-            }
-            const f32x4 dv =
-                *reinterpret_cast<const f32x4 *>(Nb + block_of(i, i) * 320 + lr * 20 + lg * 4);
-            f32x4 Y = none;
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                Y = __builtin_amdgcn_mfma_f32_16x16x4f32(dv[r], -X[r], Y, 0, 0, 0);
-            T[i] = Y;
-            store_t(i, Y);
+            for (int i = c + 1; i < 4; ++i) X[i] = times(i, c, t, X[i]);
+            t = -times(c + 1, c + 1, X[c + 1], none);
+            store_t(c + 1, t);
         }
     }
     __syncthreads();  // 3: T and the transposed values are there
