@@ -38,7 +38,7 @@ struct DeltaSeqs {
 
 // The chunked form.
 constexpr int kDeltaChunk = 64;             // tokens a chunk
-constexpr int kDeltaItemBytes = 131072;     // workspace of a chunk and head
+constexpr int kDeltaItemBytes = 107520;     // workspace of a chunk and head
 constexpr int kDeltaLds = 81920;            // LDS of a workgroup: two a compute unit
 
 // A segment of the chunks: which to prepare, and which sequences to carry on.
@@ -55,7 +55,8 @@ hipError_t launch_delta_steps(const DeltaArgs &a, const DeltaSeqs &s, bool head_
 // The scan of one segment and the preparation of the next (either may be
 // empty) in one launch.
 hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
-                               const DeltaSegment &prep, bool head_gate, hipStream_t st);
+                               const DeltaSegment &prep, bool head_gate, int cus,
+                               hipStream_t st);
 // Allow the chunk kernels their LDS on the current device.
 hipError_t allow_delta_lds();
 

@@ -72,7 +72,7 @@ constexpr int kShortRows = 16;
 
 // Chunks and heads a segment prepares at a time: enough workgroups to fill
 // the device, and two workspaces that stay inside the memory-side cache.
-constexpr long kSegmentItems = 1024;
+constexpr long kSegmentItems = 2048;
 
 struct Tables {
     std::vector<int> words;                 // every table, one after another
@@ -311,7 +311,7 @@ int proj_delta_run(const proj_delta_plan_t *p, const proj_delta_io_t *io, void *
         const DeltaSegment none{};
         const DeltaSegment &scan = i ? p->segments[i - 1] : none;
         const DeltaSegment &prep = i < n ? p->segments[i] : none;
-        e = launch_delta_chunks(a, scan, prep, io->head_gate, st);
+        e = launch_delta_chunks(a, scan, prep, io->head_gate, p->cus, st);
     }
     if (e != hipSuccess) {
         (void)hipGetLastError();

@@ -9,23 +9,24 @@
 //     o_i = S^T (q_i e^{G_i}) + sum_{j<=i} P_ij u_j,   P_ij as A with q_i,
 //     S'  = diag(e^{G_64}) S + sum_j (k_j e^{G_64 - G_j}) u_j^T.
 // With N = diag(beta) A (strictly lower triangular) and T = (1 + N)^-1
-// diag(beta), the u_i are U = T V - (T K e^G) S.  Everything but the terms
-// in S is independent of the chunks before, so the work is in two parts:
-//   prepare (one workgroup a chunk and head): W = -T K e^G, U0 = T V, P,
-//     Q e^G, K e^{G_64 - G} and e^{G_64}, written to a workspace;
-//   scan (eight waves a head, 16 columns of the state each): chunk after chunk,
-//     U = U0 + W S, O = (Q e^G) S + P U, S' as above.
+// diag(beta), the u_i are U = T R, R = V - (K e^G) S.  Only R depends on the
+// chunks before, so the work is in two parts:
+//   prepare (one workgroup a chunk and head): K e^G, Q e^G, M = (K e^{G_64 -
+//     G})^T T, P T and e^{G_64}, and V in operand order, to a workspace;
+//   scan (workgroups of four waves, 64 or 32 columns of a head's state each):
+//     chunk after chunk R = V - (K e^G) S, O = (Q e^G) S + (P T) R,
+//     S' = diag(e^{G_64}) S + M R.
 //
 // Numbers.  All products run on the 16-bit matrix cores with FP32 sums, and
 // what reaches the state is as exact as FP32 operands would make it.  Keys
 // and queries have unit length here (the chunked form is taken with l2norm
-// only), so every update is a contraction and T, W, K e^.. and Q e^.. stay
+// only), so every update is a contraction, and T, M, K e^.. and Q e^.. stay
 // within 1: they are held as two FP16 values hi + lo of 2^10 times the value,
 // and hi hi + hi lo + lo hi summed, which drops 2^-23 of each (two BF16
-// values would drop 2^-17, one 2^-9).  S, U and V have any range: a wave
-// scales what it holds by a power of two that brings the largest magnitude
-// to 2^14.  What only reaches the BF16 output (Q, P, and the hi parts of S
-// and U against them) is one FP16 value each, 2^-12.
+// values would drop 2^-17, one 2^-9).  S and R have any range: they are
+// scaled by a power of two under which a bound of their largest magnitude is
+// 2^14.  What only reaches the BF16 output (Q, P T, and the hi parts of S and
+// R against them) is one FP16 value each, 2^-12.
 // Decays are products of factors e^x with x <= 0, the sums x taken inside
 // blocks of 16 tokens from the token outward, so none is a difference of
 // large numbers: with block a after block b, e^{G_i - G_j} = (e^{sum of a's
@@ -41,12 +42,11 @@
 // the tokens of a block are scans over 16 lanes (DPP).  Operands over tokens
 // need the transpose, which a product with a selection matrix gives exactly
 // (accumulator lane l holds rows 4 (l / 16) + 0..3 of column l % 16).  The
-// order of the 32 summed values of a product is free, so the scan feeds its
-// accumulators S and U back as operands without any exchange: S tile 2 s + h
-// has channel 32 s + 8 (r / 4) + 4 h + r % 4 as row r, and a step over tokens
-// takes blocks 2 t and 2 t + 1, tokens 4 (l / 16) + 0..3 of each.  The
-// workspace holds every operand in that order, so each load is 16 bytes a
-// lane, 1 KB in one piece.
+// order of the 32 summed values of a product is free, so accumulators are fed
+// back as operands without any exchange of lanes: S tile 2 s + h has channel
+// 32 s + 8 (r / 4) + 4 h + r % 4 as row r, and a step over tokens takes blocks
+// 2 t and 2 t + 1, tokens 4 (l / 16) + 0..3 of each.  The workspace holds
+// every operand in that order, 16 bytes a lane, 1 KB in one piece.
 #include "delta.hpp"
 
 #include "device.hpp"
@@ -57,39 +57,34 @@ namespace {
 
 constexpr int kC = kDeltaChunk;   // tokens a chunk
 
-// Workspace of a chunk and head: eight pieces of 12 KB, in the order the scan
-// takes them, then U0.  Everything in operand order, 16 bytes a lane:
-//   piece it = 0..3:      W of token tile it [4 s][hi, lo], Q e^G [4 s]
-//   piece 4 + s, s = 0..3: K e^{G_64 - G} of channel tiles 2 s, 2 s + 1 [2 steps]
-//                         [hi, lo], P of token tile s [2 steps], and (s = 0)
-//                         e^{G_64} [128] FP32
-//   U0:                   [4 token tiles][8 value tiles] FP32
-constexpr int kPiece = 12288;
-constexpr int kWsU = 8 * kPiece;
-static_assert(kWsU + 32768 == kDeltaItemBytes, "workspace of an item");
-constexpr int ws_w(int it, int s) { return it * kPiece + s * 2048; }
-constexpr int ws_q(int it, int s) { return it * kPiece + 8192 + s * 1024; }
-constexpr int ws_k(int tile, int step) {
-    return (4 + tile / 2) * kPiece + (tile % 2 * 2 + step) * 2048;
-}
-constexpr int ws_p(int it, int step) { return (4 + it) * kPiece + 8192 + step * 1024; }
-constexpr int kWsD = 4 * kPiece + 8192 + 2048;
+// Workspace of a chunk and head: what wave w of the scan takes, together.
+//   token tile w:        -K e^G [4 s][hi, lo], Q e^G [4 s], V [8 value tiles] (8 bytes a lane),
+//                        P T [2 steps]
+//   channel tiles 2 w + h: M [2 h][2 steps][hi, lo]
+// then e^{G_64} [128] and the largest |v| of each token tile [4].
+constexpr int kWsWave = 26624;
+constexpr int ws_k(int s) { return s * 2048; }
+constexpr int ws_q(int s) { return 8192 + s * 1024; }
+constexpr int ws_v(int vt) { return 12288 + vt * 512; }
+constexpr int ws_p(int step) { return 16384 + step * 1024; }
+constexpr int ws_m(int h, int step) { return 18432 + (h * 2 + step) * 2048; }
+constexpr int kWsD = 4 * kWsWave;
+constexpr int kWsTop = kWsD + 512;
+static_assert(kWsTop + 512 == kDeltaItemBytes, "workspace of an item");
 
 // LDS of `prepare`, in bytes.
-constexpr int kLdsKr = 0;                     // [48 rows][hi, lo][128] FP16, dead after barrier 2
-constexpr int kLdsT = 0;                      // [hi, lo][10 blocks][16 rows][40]
-constexpr int kLdsV = kLdsT + 2 * 10 * 640;   // [8 value tiles][2 steps][64][16]
-constexpr int kLdsK = kLdsV + 16384;          // [8 channel tiles][2 steps][hi, lo][64][16]
+constexpr int kLdsKr = 0;                     // [48 rows][hi, lo][128] FP16
+constexpr int kLdsK = kLdsKr + 48 * 512;      // [8 channel tiles][2 steps][hi, lo][64][16]
 constexpr int kLdsN = kLdsK + 32768;          // [10 blocks][16 rows][20] FP32
-constexpr int kLdsTot = kLdsN + 10 * 1280;    // [4][128] FP32: a block's whole decay
+constexpr int kLdsP = kLdsN + 10 * 1280;      // [10 blocks][64][8]
+constexpr int kLdsTot = kLdsP + 10 * 512;     // [4][128] FP32: a block's whole decay
 constexpr int kLdsBeta = kLdsTot + 2048;      // [64] FP32
-constexpr int kLdsTop = kLdsBeta + 256;       // [4] largest |v| of a block (bits)
-static_assert(kLdsKr + 48 * 512 <= kLdsK, "the transposed values reuse the key rows");
-static_assert(kLdsTop + 16 <= kDeltaLds, "LDS of prepare");
-// LDS of `scan`: a ring of piece slots, each with the wave's U0 tiles behind.
-constexpr int kSlots = 5;
-constexpr int kSlot = kPiece + 4096;
-static_assert(kSlots * kSlot <= kDeltaLds, "LDS of scan");
+static_assert(kLdsBeta + 256 <= kDeltaLds, "LDS of prepare");
+// LDS of `scan` with CT column tiles.
+constexpr int lds_s(int ct, int s, int v) { return (s * ct + v) * 2048; }
+constexpr int lds_r(int ct, int st, int v) { return ct * 8192 + (st * ct + v) * 2048; }
+constexpr int lds_tops(int ct) { return ct * 12288; }  // of S [4], of R [4]
+static_assert(lds_tops(4) + 32 <= kDeltaLds, "LDS of scan");
 
 typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
 
@@ -140,11 +135,6 @@ __device__ __forceinline__ float h_lo(unsigned u) {
 __device__ __forceinline__ float h_hi(unsigned u) {
     return (float)__builtin_bit_cast(_Float16, (uint16_t)(u >> 16));
 }
-
-template <int I>
-struct Place {
-    static constexpr int value = I;
-};
 
 // The bits v as they are: without this the compiler may round a product to
 // FP16 twice, once fused with the product and once after its FP32 rounding,
@@ -259,15 +249,15 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 
     // ---- this lane's token: keys, queries, values, gates
     const u32x4 zero = {0u, 0u, 0u, 0u};
-    u32x4 kv[4], qv[4], vv[4], fv[4];
+    char *wsw = ws + w * kWsWave;
+    u32x4 kv[4], qv[4], fv[4];
 #pragma unroll
     for (int s = 0; s < 4; ++s) {
         const int c = 32 * s + 8 * lg;
-        kv[s] = qv[s] = vv[s] = fv[s] = zero;
+        kv[s] = qv[s] = fv[s] = zero;
         if (live) {
             kv[s] = *reinterpret_cast<const u32x4 *>(a.k + row * a.ldk + hk * kHead + c);
             qv[s] = *reinterpret_cast<const u32x4 *>(a.q + row * a.ldq + hk * kHead + c);
-            vv[s] = *reinterpret_cast<const u32x4 *>(a.v + row * a.ldv + h * kHead + c);
             if constexpr (!HEAD_GATE)
                 fv[s] = *reinterpret_cast<const u32x4 *>(a.f + row * a.ldf + h * kHead + c);
         }
@@ -361,20 +351,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
         }
     }
     const bool mild = __all(least > -kMild);
-    {
-        unsigned top = 0;
-#pragma unroll
-        for (int s = 0; s < 4; ++s)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const unsigned lo = (vv[s][i] << 16) & 0x7FFFFFFFu, hi = vv[s][i] & 0x7FFF0000u;
-                top = lo > top ? lo : top;
-                top = hi > top ? hi : top;
-            }
-        top = max64(top);
-        if (lane == 0) reinterpret_cast<unsigned *>(lds + kLdsTop)[w] = top;
-    }
-    __syncthreads();  // 1: key rows, block totals, betas and the values' range are there
+    __syncthreads();  // 1: key rows, block totals and betas are there
 
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
     unsigned pick0 = 0, pick1 = 0;  // FP16 one for channel lr % 4 of four, in its lane group
@@ -416,34 +393,33 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             x[e] = kf[e] * el[s][e];
             y[e] = qf[e] * rq * el[s][e];
         }
-        // to the chunk's ends: Q e^G and K e^{G_64 - G} to the workspace, K e^G to LDS
+        // to the chunk's ends: K e^G and Q e^G to the workspace, K e^{G_64 - G} to LDS
         {
             float kt[8], kh[8], qt[8];
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                kt[e] = x[e] * before[e / 4][e % 4];
+                kt[e] = -x[e] * before[e / 4][e % 4];
                 qt[e] = y[e] * before[e / 4][e % 4];
                 kh[e] = kf[e] * er[s][e] * behind[e / 4][e % 4];
             }
-            *reinterpret_cast<u32x4 *>(ws + ws_q(0, s) + w * kPiece + lane * 16) = round_h(qt);
+            *reinterpret_cast<u32x4 *>(wsw + ws_q(s) + lane * 16) = round_h(qt);
             if (w == 3 && lr == 15) {  // e^{G_64}: the decay of the whole chunk
                 f32x4 *o = reinterpret_cast<f32x4 *>(ws + kWsD + c * 4);
                 o[0] = f32x4{el[s][0], el[s][1], el[s][2], el[s][3]} * before[0];
                 o[1] = f32x4{el[s][4], el[s][5], el[s][6], el[s][7]} * before[1];
             }
             const Split st = split_h(kt), sh = split_h(kh);
+            *reinterpret_cast<u32x4 *>(wsw + ws_k(s) + lane * 16) = st.hi;
+            *reinterpret_cast<u32x4 *>(wsw + ws_k(s) + 1024 + lane * 16) = st.lo;
 #pragma unroll
             for (int hf = 0; hf < 2; ++hf) {
                 // column r of the selection picks channel 8 (r / 4) + 4 hf + r % 4
                 const u32x4 sel =
                     hf ? u32x4{0u, 0u, pick0, pick1} : u32x4{pick0, pick1, 0u, 0u};
-                const int half = lane * 16 + (w & 1) * 8;
-                char *kl = lds + kLdsK + ((2 * s + hf) * 2 + (w >> 1)) * 2048 + half;
-                char *kg = ws + ws_k(2 * s + hf, 0) + (w >> 1) * 2048 + half;
-                *reinterpret_cast<u32x2 *>(kl) = pack4_h(mfma_h(st.hi, sel, none));
-                *reinterpret_cast<u32x2 *>(kl + 1024) = pack4_h(mfma_h(st.lo, sel, none));
-                *reinterpret_cast<u32x2 *>(kg) = pack4_h(mfma_h(sh.hi, sel, none));
-                *reinterpret_cast<u32x2 *>(kg + 1024) = pack4_h(mfma_h(sh.lo, sel, none));
+                char *to = lds + kLdsK + ((2 * s + hf) * 2 + (w >> 1)) * 2048 + lane * 16 +
+                           (w & 1) * 8;
+                *reinterpret_cast<u32x2 *>(to) = pack4_h(mfma_h(sh.hi, sel, none));
+                *reinterpret_cast<u32x2 *>(to + 1024) = pack4_h(mfma_h(sh.lo, sel, none));
             }
         }
         // A and P, block row w: inside the block, then the blocks before
@@ -565,9 +541,8 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             if (b == w && 4 * lg + r > lr) Pb[r] = 0.f;   // on it and below
             blk[(4 * lg + r) * 20 + lr] = Ab[r] * beta4[r];
         }
-        char *po = ws + ws_p(0, b >> 1) + w * kPiece + lane * 16;
-        *reinterpret_cast<u32x2 *>(po + (b & 1) * 8) = pack4_h(Pb * (1.f / kUnit));
-        if (b == w && (b & 1) == 0) *reinterpret_cast<u32x2 *>(po + 8) = u32x2{0u, 0u};
+        *reinterpret_cast<u32x2 *>(lds + kLdsP + block_of(w, b) * 512 + lane * 8) =
+            pack4_h(Pb * (1.f / kUnit));
     }
     // ---- inverse of this block's 1 + N by forward substitution, a column a lane
     {
@@ -586,15 +561,41 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
             for (int i = 0; i < 16; ++i) blk[i * 20 + lr] = x[i];
     }
-    __syncthreads();  // 2: N below the diagonal and the inverses are there; key rows are free
+    u32x4 vv[4];
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+        vv[s] = live ? *reinterpret_cast<const u32x4 *>(a.v + row * a.ldv + h * kHead + 32 * s +
+                                                        8 * lg)
+                     : zero;
+    __syncthreads();  // 2: N below the diagonal, the inverses, P and K e^{G_64 - G} are there
 
-    // ---- V transposed (scaled to FP16's range), and column block w of the whole inverse
-    Scale sv;
+    // ---- column block w of T, a block at a time: T_ww is the block's inverse,
+    // T_aw = -(inverse of a) (sum_c N_ac T_cw); rows i = 4 lg + r, column lr
+    f32x4 T[4] = {none, none, none, none};
     {
-        const u32x4 t = *reinterpret_cast<const u32x4 *>(lds + kLdsTop);
-        const unsigned x = t.x > t.y ? t.x : t.y, y = t.z > t.w ? t.z : t.w;
-        sv = scale_for(x > y ? x : y);
+        auto times = [&](int ai, int bi, f32x4 t, f32x4 acc) {  // block (ai, bi) of N times t
+            const f32x4 nv =
+                *reinterpret_cast<const f32x4 *>(Nb + block_of(ai, bi) * 320 + lr * 20 + lg * 4);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(nv[r], t[r], acc, 0, 0, 0);
+            return acc;
+        };
+        const float *d = Nb + block_of(w, w) * 320;
+        f32x4 t, X[4] = {none, none, none, none};
+#pragma unroll
+        for (int r = 0; r < 4; ++r) t[r] = d[(4 * lg + r) * 20 + lr];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c < w) continue;  // uniform
+            T[c] = t;
+#pragma unroll
+            for (int i = c + 1; i < 4; ++i) X[i] = times(i, c, t, X[i]);
+            if (c < 3) t = -times(c < 3 ? c + 1 : 3, c < 3 ? c + 1 : 3, X[c < 3 ? c + 1 : 3], none);
+        }
     }
+    // ---- V in operand order: transposed, its own BF16 values
+    unsigned top = 0;
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
@@ -605,284 +606,270 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
-            *reinterpret_cast<u32x2 *>(lds + kLdsV + ((2 * s + hf) * 2 + (w >> 1)) * 1024 +
-                                       lane * 16 + (w & 1) * 8) =
-                pack4_h(mfma_bf(vv[s], sel, none) * sv.up);
+            const f32x4 x = mfma_bf(vv[s], sel, none);
+            top = top_of(x, top);
+            *reinterpret_cast<u32x2 *>(wsw + ws_v(2 * s + hf) + lane * 8) =
+                u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
         }
-    {
-        const float bj = betas[w * 16 + lr] * kUnit;
-        auto store_t = [&](int ai, f32x4 t) {  // T_ab diag(beta), rows i = 4 lg + r, column lr
-            char *o = lds + kLdsT + block_of(ai, w) * 640 + lr * 2;
-#pragma unroll
-            for (int r = 0; r < 4; ++r) {
-                const float x = t[r] * bj;
-                const unsigned hi = settled(pack_h(x, 0.f));
-                *reinterpret_cast<uint16_t *>(o + (4 * lg + r) * 40) = (uint16_t)hi;
-                *reinterpret_cast<_Float16 *>(o + 6400 + (4 * lg + r) * 40) =
-                    (_Float16)(x - h_lo(hi));
-            }
-        };
-        auto times = [&](int ai, int bi, f32x4 t, f32x4 acc) {  // block (ai, bi) of N times t
-            const f32x4 nv =
-                *reinterpret_cast<const f32x4 *>(Nb + block_of(ai, bi) * 320 + lr * 20 + lg * 4);
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-                acc = __builtin_amdgcn_mfma_f32_16x16x4f32(nv[r], t[r], acc, 0, 0, 0);
-            return acc;
-        };
-        // T_ww is the block's inverse; T_aw = -(inverse of a) (sum_c N_ac T_cw)
-        const float *d = Nb + block_of(w, w) * 320;
-        f32x4 t, X[4] = {none, none, none, none};
-#pragma unroll
-        for (int r = 0; r < 4; ++r) t[r] = d[(4 * lg + r) * 20 + lr];
-        store_t(w, t);
-#pragma unroll
-        for (int c = 0; c < 3; ++c) {
-            if (c < w) continue;  // uniform
-#pragma unroll
-            for (int i = c + 1; i < 4; ++i) X[i] = times(i, c, t, X[i]);
-            t = -times(c + 1, c + 1, X[c + 1], none);
-            store_t(c + 1, t);
-        }
-    }
-    __syncthreads();  // 3: T and the transposed values are there
+    top = max64(top);
+    if (lane == 0) reinterpret_cast<unsigned *>(ws + kWsTop)[w] = top;
 
-    // ---- W = -T K e^G (channels 32 w + 0..31) and U0 = T V (the same columns)
-    f32x4 Wt[2][4], U[4][2];  // W^T[channel tile][token tile], U0[token tile][value tile]
+    // ---- columns of block w of M (as M^T: tokens j = 4 lg + r, channel lr of a tile) and of P T
+    const float bj = betas[w * 16 + lr] * kUnit;
+    const Split t0 = split_h(T[0], T[1], bj), t1 = split_h(T[2], T[3], bj);
+    const int half = lane * 16 + (w & 1) * 8, step = w >> 1;
+#pragma unroll
+    for (int t = 0; t < 8; ++t) {
+        f32x4 x = none, y = none;
+#pragma unroll
+        for (int st = 0; st < 2; ++st) {
+            if (st < step) continue;  // T is zero there; uniform
+            const char *kp = lds + kLdsK + (t * 2 + st) * 2048 + lane * 16;
+            const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
+            const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
+            const Split &ts = st ? t1 : t0;
+            x = mfma_h(ts.hi, kl, x);
+            y = mfma_h(ts.hi, kh, y);
+            x = mfma_h(ts.lo, kh, x);
+        }
+        float m[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) m[r] = (x[r] + y[r]) * (1.f / kUnit);
+        const unsigned h0 = settled(pack_h(m[0], m[1])), h1 = settled(pack_h(m[2], m[3]));
+        char *to = ws + (t >> 1) * kWsWave + ws_m(t & 1, 0) + step * 2048 + half;
+        *reinterpret_cast<u32x2 *>(to) = u32x2{h0, h1};
+        *reinterpret_cast<u32x2 *>(to + 1024) =
+            u32x2{pack_h(m[0] - h_lo(h0), m[1] - h_hi(h0)),
+                  pack_h(m[2] - h_lo(h1), m[3] - h_hi(h1))};
+    }
 #pragma unroll
     for (int it = 0; it < 4; ++it) {
+        if (it >> 1 < step) continue;  // the scan does not read these; uniform
+        f32x4 x = none;
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) Wt[hf][it] = U[it][hf] = none;
-#pragma unroll
-        for (int st = 0; st <= it >> 1; ++st) {
-            const char *t0 = lds + kLdsT + block_of(it, 2 * st) * 640 + lr * 40 + lg * 8;
-            const u32x2 h0 = *reinterpret_cast<const u32x2 *>(t0);
-            const u32x2 l0 = *reinterpret_cast<const u32x2 *>(t0 + 6400);
-            u32x2 h1 = {0u, 0u}, l1 = {0u, 0u};
-            if (2 * st + 1 <= it) {
-                h1 = *reinterpret_cast<const u32x2 *>(t0 + 640);
-                l1 = *reinterpret_cast<const u32x2 *>(t0 + 640 + 6400);
-            }
-            const u32x4 th = {h0.x, h0.y, h1.x, h1.y}, tl = {l0.x, l0.y, l1.x, l1.y};
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const char *kp = lds + kLdsK + ((2 * w + hf) * 2 + st) * 2048 + lane * 16;
-                const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
-                const u32x4 ko = *reinterpret_cast<const u32x4 *>(kp + 1024);
-                const u32x4 vt = *reinterpret_cast<const u32x4 *>(
-                    lds + kLdsV + ((2 * w + hf) * 2 + st) * 1024 + lane * 16);
-                Wt[hf][it] = mfma_h(kh, tl, Wt[hf][it]);
-                Wt[hf][it] = mfma_h(ko, th, Wt[hf][it]);
-                Wt[hf][it] = mfma_h(kh, th, Wt[hf][it]);
-                U[it][hf] = mfma_h(tl, vt, U[it][hf]);
-                U[it][hf] = mfma_h(th, vt, U[it][hf]);
-            }
+        for (int st = 0; st < 2; ++st) {
+            if (st < step || 2 * st > it) continue;  // uniform
+            const char *pp = lds + kLdsP + block_of(it, 2 * st) * 512 + lane * 8;
+            const u32x2 p0 = *reinterpret_cast<const u32x2 *>(pp);
+            u32x2 p1 = {0u, 0u};
+            if (2 * st + 1 <= it) p1 = *reinterpret_cast<const u32x2 *>(pp + 512);
+            x = mfma_h((st ? t1 : t0).hi, u32x4{p0.x, p0.y, p1.x, p1.y}, x);
         }
-        const Split o = split_h(Wt[0][it], Wt[1][it], -1.f / kUnit);
-        char *wp = ws + ws_w(it, 0) + w * 2048 + lane * 16;
-        *reinterpret_cast<u32x4 *>(wp) = o.hi;
-        *reinterpret_cast<u32x4 *>(wp + 1024) = o.lo;
-        const float back = sv.down / kUnit;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-            *reinterpret_cast<f32x4 *>(ws + kWsU + ((it * 8 + 2 * w + hf) * 64 + lane) * 16) =
-                U[it][hf] * back;
+        *reinterpret_cast<u32x2 *>(ws + it * kWsWave + ws_p(0) + step * 1024 + half) =
+            pack4_h(x * (1.f / kUnit));
     }
 }
 
 // ---------------------------------------------------------------------------
-// scan: a workgroup of four waves a head and 64 columns of its state, 16
-// columns a wave, chunk after chunk.  A chunk's eight pieces go straight into
-// a ring of LDS slots (global_load_lds_dwordx4), kSlots - 1 pieces ahead,
-// and every wave reads its operands from there, so the state, which the next
-// chunk waits for, never waits for memory.  One barrier a piece.
+// scan: a workgroup of four waves a head and 16 * CT columns of its state,
+// chunk after chunk.  Wave w holds channel tiles 2 w and 2 w + 1 of S and
+// computes token tile w of R and O, so each operand from the workspace goes
+// to one wave only, straight into registers (those of the next chunk are
+// loaded as soon as this one's are used); S and R meet in LDS as FP16 pairs.
+// Two barriers a chunk.
+//
+// The scales of S and R are common to the waves without another exchange:
+// |R| <= max |v| + sqrt(128) max |S| (|k e^G| <= 1), and the S of the next
+// chunk is at most max |S| + 64 max |R|; both maxima come with the operands.
 // ---------------------------------------------------------------------------
-#pragma clang diagnostic push
-#pragma clang diagnostic ignored "-Winline-asm"
-// 16 bytes a lane from src into LDS at base + 16 * lane (base uniform).  M0
-// needs one wait state between its write and the load that reads it.
-__device__ __forceinline__ void lds_load16(const void *src, uint32_t base) {
-    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off"
-                 :
-                 : "v"(src), "s"(base)
-                 : "memory", "m0");
+__device__ __forceinline__ Scale scale_below(float bound) {
+    return scale_for(__float_as_uint(fminf(bound, 3e38f)));
 }
-#pragma clang diagnostic pop
-
-// A wave's loads of piece p: a quarter of the piece, and with W its own
-// columns of U0.
-constexpr int piece_loads(int p) { return p % 8 < 4 ? 4 : 3; }
-// Loads of the kSlots - 2 pieces after piece p, which may be in flight when
-// piece p is needed.
-constexpr int loads_after(int p) {
-    int n = 0;
-    for (int i = 1; i <= kSlots - 2; ++i) n += piece_loads(p + i);
-    return n;
+__device__ __forceinline__ float largest(u32x4 t) {
+    const unsigned x = t.x > t.y ? t.x : t.y, y = t.z > t.w ? t.z : t.w;
+    return __uint_as_float(x > y ? x : y);
 }
 
-__device__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot, int h, int part,
-                             const char *ws, size_t ws_step, char *lds) {
+template <int CT>
+__device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot,
+                                             int h, int part, const char *ws, size_t ws_step,
+                                             char *lds) {
     const int lane = threadIdx.x & 63;
     const int w = scalar(threadIdx.x >> 6);
     const int lr = lane & 15, lg = lane >> 4;
-    const int vt = part * 4 + w;  // this wave's value tile
-    const int chunks = (rows + kC - 1) / kC;
-    const uint32_t lds0 =
-        scalar((int)(uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void *)lds);
-    float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) + vt * 16 + lr;
-    f32x4 S[8];
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r)
-            S[t][r] = state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead];
-    wait_loads<0>();  // the ring's loads are counted from here
-
-    // the next piece to load: its place in the chunk is known where it is issued
-    int slot_in = 0, chunk_in = 0;
-    const char *ws_in = ws;
-    auto issue = [&](int p) {  // p: place of the piece in its chunk
-        const uint32_t to = lds0 + (uint32_t)(slot_in * kSlot);
-        const char *from = ws_in + p * kPiece + w * 3072 + lane * 16;
-#pragma unroll
-        for (int j = 0; j < 3; ++j)
-            lds_load16(from + j * 1024, to + (uint32_t)(w * 3072 + j * 1024));
-        if (p < 4)
-            lds_load16(ws_in + kWsU + (p * 8 + vt) * 1024 + lane * 16,
-                       to + (uint32_t)(kPiece + w * 1024));
-        slot_in = slot_in + 1 == kSlots ? 0 : slot_in + 1;
-        // past the last chunk the ring reads it again: nothing uses that
-        if (p == 7 && ++chunk_in < chunks) ws_in += ws_step;
-    };
-#pragma unroll
-    for (int p = 0; p < kSlots - 1; ++p) issue(p);
-
-    int slot_at = 0;
-    const char *in = lds;
-    auto next = [&](auto place) {  // piece `place` of the chunk has landed, the one before is free
-        constexpr int p = decltype(place)::value;
-        wait_loads<loads_after(p)>();
-        __syncthreads();
-        issue((p + kSlots - 1) % 8);
-        in = lds + slot_at * kSlot;
-        slot_at = slot_at + 1 == kSlots ? 0 : slot_at + 1;
-    };
-
     const f32x4 none = {0.f, 0.f, 0.f, 0.f};
+    unsigned *tops = reinterpret_cast<unsigned *>(lds + lds_tops(CT));
+    float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) +
+                   (size_t)(32 * w + 8 * lg) * kHead + part * (16 * CT) + lr;
+    f32x4 S[2][CT];
+    unsigned top = 0;
+#pragma unroll
+    for (int hf = 0; hf < 2; ++hf)
+#pragma unroll
+        for (int v = 0; v < CT; ++v) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) S[hf][v][r] = state[(4 * hf + r) * kHead + v * 16];
+            top = top_of(S[hf][v], top);
+        }
+    // a chunk's operands of this wave
+    Split kf[4], mf[2][2];
+    u32x4 qf[4], pf[2], vtop;
+    u32x2 vf[CT];
+    f32x4 df[2];
+    auto load_first = [&](const char *at) {  // what R takes
+        const char *from = at + w * kWsWave + lane * 16;
+#pragma unroll
+        for (int s = 0; s < 4; ++s) {
+            kf[s].hi = *reinterpret_cast<const u32x4 *>(from + ws_k(s));
+            kf[s].lo = *reinterpret_cast<const u32x4 *>(from + ws_k(s) + 1024);
+            qf[s] = *reinterpret_cast<const u32x4 *>(from + ws_q(s));
+        }
+#pragma unroll
+        for (int v = 0; v < CT; ++v)
+            vf[v] = *reinterpret_cast<const u32x2 *>(at + w * kWsWave + ws_v(0) +
+                                                     (part * CT + v) * 512 + lane * 8);
+        vtop = *reinterpret_cast<const u32x4 *>(at + kWsTop);
+    };
+    auto load_second = [&](const char *at) {  // what S takes
+        const char *from = at + w * kWsWave + lane * 16;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                mf[hf][st].hi = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st));
+                mf[hf][st].lo = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st) + 1024);
+            }
+            df[hf] = *reinterpret_cast<const f32x4 *>(at + kWsD + (32 * w + 8 * lg + 4 * hf) * 4);
+        }
+        pf[0] = *reinterpret_cast<const u32x4 *>(from + ws_p(0));
+        if (w >= 2) pf[1] = *reinterpret_cast<const u32x4 *>(from + ws_p(1));
+    };
+    load_first(ws);
+    load_second(ws);
+
+    auto share = [&](float up) {  // this wave's channels of S, as operands of step s = w
+#pragma unroll
+        for (int v = 0; v < CT; ++v) {
+            const Split x = split_h(S[0][v], S[1][v], up);
+            char *to = lds + lds_s(CT, w, v) + lane * 16;
+            *reinterpret_cast<u32x4 *>(to) = x.hi;
+            *reinterpret_cast<u32x4 *>(to + 1024) = x.lo;
+        }
+    };
+    top = max64(top);
+    if (lane == 0) tops[w] = top;
+    __syncthreads();
+    Scale ss = scale_below(largest(*reinterpret_cast<const u32x4 *>(tops)));
+    share(ss.up);
+
     for (int r0 = 0; r0 < rows; r0 += kC) {
         const int n = min(kC, rows - r0);
-        unsigned top = 0;
+        const char *next = r0 + kC < rows ? ws + ws_step : ws;  // past the end: read again, unused
+        __syncthreads();  // S and its maxima are there
+        const float smax = largest(*reinterpret_cast<const u32x4 *>(tops));
+        const Scale sr = scale_below(largest(vtop) + 12.f * smax);
+        f32x4 x[CT], y[CT], o[CT];
 #pragma unroll
-        for (int t = 0; t < 8; ++t) top = top_of(S[t], top);
-        const Scale ss = scale_for(max64(top));
+        for (int v = 0; v < CT; ++v) x[v] = y[v] = o[v] = none;
+#pragma unroll
+        for (int s = 0; s < 4; ++s)
+#pragma unroll
+            for (int v = 0; v < CT; ++v) {
+                const char *at = lds + lds_s(CT, s, v) + lane * 16;
+                const u32x4 bh = *reinterpret_cast<const u32x4 *>(at);
+                const u32x4 bl = *reinterpret_cast<const u32x4 *>(at + 1024);
+                x[v] = mfma_h(kf[s].hi, bl, x[v]);
+                y[v] = mfma_h(kf[s].hi, bh, y[v]);
+                o[v] = mfma_h(bh, qf[s], o[v]);
+                x[v] = mfma_h(kf[s].lo, bh, x[v]);
+            }
         const float back = ss.down / kUnit;
-        Split b[4];
-#pragma unroll
-        for (int s = 0; s < 4; ++s) b[s] = split_h(S[2 * s], S[2 * s + 1], ss.up);
-        f32x4 U[4], O[4];  // U[token][value]; O[value][token] of Q S
         top = 0;
-        auto rows_of = [&](auto tile) {
-            constexpr int it = decltype(tile)::value;
-            next(tile);
-            const char *at = in + lane * 16;
-            f32x4 x = none, y = none, z = none, o = none;
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-                const u32x4 wh = *reinterpret_cast<const u32x4 *>(at + s * 2048);
-                const u32x4 wl = *reinterpret_cast<const u32x4 *>(at + s * 2048 + 1024);
-                const u32x4 q = *reinterpret_cast<const u32x4 *>(at + 8192 + s * 1024);
-                x = mfma_h(wh, b[s].lo, x);
-                y = mfma_h(wl, b[s].hi, y);
-                z = mfma_h(wh, b[s].hi, z);
-                o = mfma_h(b[s].hi, q, o);
-            }
-            O[it] = o;
-            const f32x4 u0 = *reinterpret_cast<const f32x4 *>(at + kPiece + w * 1024);
+        for (int v = 0; v < CT; ++v) {
+            const float vv[4] = {bf16_lo(vf[v].x), bf16_hi(vf[v].x), bf16_lo(vf[v].y),
+                                 bf16_hi(vf[v].y)};
+            f32x4 R;
 #pragma unroll
-            for (int r = 0; r < 4; ++r)
-                U[it][r] = __builtin_fmaf((x[r] + y[r]) + z[r], back, u0[r]);
-            top = top_of(U[it], top);
-        };
-        rows_of(Place<0>{});
-        rows_of(Place<1>{});
-        rows_of(Place<2>{});
-        rows_of(Place<3>{});
-        const Scale su = scale_for(max64(top));
-        const float ub = su.down / kUnit;
-        const float os = back * a.scale, ou = ub * a.scale;
-        const Split u[2] = {split_h(U[0], U[1], su.up), split_h(U[2], U[3], su.up)};
-        auto channels_of = [&](auto quarter) {
-            constexpr int q = decltype(quarter)::value;
-            next(Place<4 + q>{});
-            const char *at = in + lane * 16;
-            if (q == 0) {
-                // the whole chunk's decays, of every piece's channels
+            for (int r = 0; r < 4; ++r) R[r] = __builtin_fmaf(x[v][r] + y[v][r], back, vv[r]);
+            top = top_of(R, top);
+            R *= sr.up;
+            const unsigned h0 = settled(pack_h(R[0], R[1])), h1 = settled(pack_h(R[2], R[3]));
+            char *to = lds + lds_r(CT, 0, v) + (w >> 1) * (CT * 2048) + lane * 16 + (w & 1) * 8;
+            *reinterpret_cast<u32x2 *>(to) = u32x2{h0, h1};
+            *reinterpret_cast<u32x2 *>(to + 1024) =
+                u32x2{pack_h(R[0] - h_lo(h0), R[1] - h_hi(h0)),
+                      pack_h(R[2] - h_lo(h1), R[3] - h_hi(h1))};
+        }
+        load_first(next);
+        top = max64(top);
+        if (lane == 0) tops[4 + w] = top;
+        __syncthreads();  // R and its maxima are there; S's operands are free
+        const float bound = smax + 64.f * largest(*reinterpret_cast<const u32x4 *>(tops + 4));
+        f32x4 u[2][CT], z[2][CT], ou[CT];
 #pragma unroll
-                for (int t = 0; t < 8; ++t) {
-                    const f32x4 d = *reinterpret_cast<const f32x4 *>(
-                        in + (kWsD - 4 * kPiece) + (32 * (t >> 1) + 8 * lg + 4 * (t & 1)) * 4);
-                    S[t] *= d;
+        for (int v = 0; v < CT; ++v) u[0][v] = u[1][v] = z[0][v] = z[1][v] = ou[v] = none;
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int v = 0; v < CT; ++v) {
+                const char *at = lds + lds_r(CT, st, v) + lane * 16;
+                const u32x4 bh = *reinterpret_cast<const u32x4 *>(at);
+                const u32x4 bl = *reinterpret_cast<const u32x4 *>(at + 1024);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    u[hf][v] = mfma_h(mf[hf][st].hi, bl, u[hf][v]);
+                    z[hf][v] = mfma_h(mf[hf][st].hi, bh, z[hf][v]);
                 }
+                if (st == 0 || w >= 2) ou[v] = mfma_h(bh, pf[st], ou[v]);
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) u[hf][v] = mfma_h(mf[hf][st].lo, bh, u[hf][v]);
             }
-            f32x4 x[2] = {none, none}, y[2] = {none, none}, o = none;
+        const float rb = sr.down / kUnit;
+        top = 0;
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const char *kp = at + (hf * 2 + st) * 2048;
-                    const u32x4 kh = *reinterpret_cast<const u32x4 *>(kp);
-                    const u32x4 kl = *reinterpret_cast<const u32x4 *>(kp + 1024);
-                    x[hf] = mfma_h(kh, u[st].lo, x[hf]);
-                    y[hf] = mfma_h(kh, u[st].hi, y[hf]);
-                    x[hf] = mfma_h(kl, u[st].hi, x[hf]);
-                }
-#pragma unroll
-            for (int st = 0; st <= q >> 1; ++st) {
-                const u32x4 p = *reinterpret_cast<const u32x4 *>(at + 8192 + st * 1024);
-                o = mfma_h(u[st].hi, p, o);
-            }
-#pragma unroll
-            for (int hf = 0; hf < 2; ++hf)
+            for (int v = 0; v < CT; ++v) {
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
-                    S[2 * q + hf][r] =
-                        __builtin_fmaf(x[hf][r] + y[hf][r], ub, S[2 * q + hf][r]);
-            if (q * 16 + lr < n) {
-                float v[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(O[q][r], os, o[r] * ou);
-                *reinterpret_cast<u32x2 *>(a.out + (size_t)(row0 + r0 + q * 16 + lr) * a.ldo +
-                                           h * kHead + vt * 16 + lg * 4) =
-                    u32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+                    S[hf][v][r] = __builtin_fmaf(u[hf][v][r] + z[hf][v][r], rb,
+                                                 S[hf][v][r] * df[hf][r]);
+                top = top_of(S[hf][v], top);
             }
-        };
-        channels_of(Place<0>{});
-        channels_of(Place<1>{});
-        channels_of(Place<2>{});
-        channels_of(Place<3>{});
+        load_second(next);
+        const float os = back * a.scale, ob = rb * a.scale;
+        ss = scale_below(bound);
+        share(ss.up);
+        top = max64(top);
+        if (lane == 0) tops[w] = top;
+        if (w * 16 + lr < n) {
+            uint16_t *to = a.out + (size_t)(row0 + r0 + w * 16 + lr) * a.ldo + h * kHead +
+                           part * (16 * CT) + lg * 4;
+#pragma unroll
+            for (int v = 0; v < CT; ++v) {
+                float e[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) e[r] = __builtin_fmaf(o[v][r], os, ou[v][r] * ob);
+                *reinterpret_cast<u32x2 *>(to + v * 16) =
+                    u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])};
+            }
+        }
+        ws = next;
     }
-    wait_loads<0>();  // no wave leaves LDS writes in flight
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int r = 0; r < 4; ++r)
-            state[(size_t)(32 * (t >> 1) + 8 * lg + 4 * (t & 1) + r) * kHead] = S[t][r];
+        for (int v = 0; v < CT; ++v)
+#pragma unroll
+            for (int r = 0; r < 4; ++r) state[(4 * hf + r) * kHead + v * 16] = S[hf][v][r];
 }
 
 // A launch holds the scan of one segment (its workgroups come first) and the
 // preparation of the next, which do not depend on each other.
-template <bool HEAD_GATE>
+template <int CT, bool HEAD_GATE>
 __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaSegment scan,
                                                              DeltaSegment prep) {
     extern __shared__ __align__(16) char lds[];
-    const int scans = scan.seqs * a.H * 2;  // two workgroups of 64 columns a head
+    constexpr int PARTS = 8 / CT;  // workgroups a head in the scan
+    const int scans = scan.seqs * a.H * PARTS;
     int i = blockIdx.x;
     if (i < scans) {
-        const int h = (i >> 1) % a.H;
-        const int *e = scan.seq_table + 4 * ((i >> 1) / a.H);
-        scan_columns(a, e[0], e[1], e[2], h, i & 1,
-                     scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
-                     (size_t)a.H * kDeltaItemBytes, lds);
+        const int h = i / PARTS % a.H;
+        const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
+        scan_columns<CT>(a, e[0], e[1], e[2], h, i % PARTS,
+                         scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                         (size_t)a.H * kDeltaItemBytes, lds);
         return;
     }
     i -= scans;
@@ -891,26 +878,38 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaS
     prepare_item<HEAD_GATE>(a, e[0], e[1], h, prep.ws + (size_t)i * kDeltaItemBytes, lds);
 }
 
-}  // namespace
-
-hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
-                               const DeltaSegment &prep, bool head_gate, hipStream_t st) {
-    const dim3 grid((unsigned)(scan.seqs * a.H * 2 + prep.chunks * a.H));
-    if (head_gate)
-        hipLaunchKernelGGL(delta_chunk_kernel<true>, grid, dim3(256), kDeltaLds, st, a, scan, prep);
-    else
-        hipLaunchKernelGGL(delta_chunk_kernel<false>, grid, dim3(256), kDeltaLds, st, a, scan,
-                           prep);
+template <int CT, bool HEAD_GATE>
+hipError_t launch(const DeltaArgs &a, const DeltaSegment &scan, const DeltaSegment &prep,
+                  hipStream_t st) {
+    const dim3 grid((unsigned)(scan.seqs * a.H * (8 / CT) + prep.chunks * a.H));
+    hipLaunchKernelGGL((delta_chunk_kernel<CT, HEAD_GATE>), grid, dim3(256), kDeltaLds, st, a,
+                       scan, prep);
     return hipGetLastError();
 }
 
+}  // namespace
+
+hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
+                               const DeltaSegment &prep, bool head_gate, int cus,
+                               hipStream_t st) {
+    // 32 columns a workgroup while those leave compute units idle, 64 above
+    const bool narrow = (long)scan.seqs * a.H * 2 <= cus / 2;
+    if (narrow)
+        return head_gate ? launch<2, true>(a, scan, prep, st) : launch<2, false>(a, scan, prep, st);
+    return head_gate ? launch<4, true>(a, scan, prep, st) : launch<4, false>(a, scan, prep, st);
+}
+
 hipError_t allow_delta_lds() {
-    const auto attr = hipFuncAttributeMaxDynamicSharedMemorySize;
-    const hipError_t e = hipFuncSetAttribute(
-        reinterpret_cast<const void *>(&delta_chunk_kernel<true>), attr, kDeltaLds);
-    if (e != hipSuccess) return e;
-    return hipFuncSetAttribute(reinterpret_cast<const void *>(&delta_chunk_kernel<false>), attr,
-                               kDeltaLds);
+    hipError_t e = hipSuccess;
+    auto one = [&](const void *f) {
+        if (e == hipSuccess)
+            e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kDeltaLds);
+    };
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, true>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, false>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<4, true>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<4, false>));
+    return e;
 }
 
 }  // namespace tp1
