@@ -45,13 +45,12 @@ namespace {
 // X(bcap, rows, waves, kw, kc, depth, nw): batch capacity, 16-row weight
 // tiles a group, waves along the batch, waves along K, K bytes a step, LDS
 // stages, waves a workgroup.
-#define TP1_I8_INSTANCES(X)                                                     \
-    X(16, 4, 1, 1, 256, 4, 4) X(16, 4, 1, 2, 512, 3, 8) X(16, 2, 1, 4, 512, 4, 8) \
-    X(16, 2, 1, 4, 1024, 3, 8) X(16, 8, 1, 1, 256, 3, 4) X(16, 1, 1, 8, 512, 4, 8) \
-    X(32, 4, 2, 1, 256, 4, 8) X(32, 8, 2, 1, 256, 3, 8) X(32, 2, 1, 4, 512, 4, 8)  \
-    X(64, 8, 2, 1, 256, 3, 8) X(64, 8, 4, 1, 256, 3, 8) X(64, 16, 2, 1, 128, 3, 8) \
-    X(64, 4, 2, 1, 256, 4, 8) X(128, 16, 2, 1, 128, 3, 8) X(128, 8, 2, 1, 128, 4, 8) \
-    X(256, 8, 4, 1, 128, 3, 8) X(256, 16, 4, 1, 64, 4, 8)
+#define TP1_I8_INSTANCES(X)                                                                \
+    X(16, 4, 1, 1, 512, 2, 4) X(16, 1, 1, 8, 512, 8, 8) X(16, 1, 1, 8, 512, 4, 8)          \
+    X(32, 8, 2, 1, 256, 3, 8) X(32, 4, 1, 2, 512, 3, 8) X(64, 16, 2, 1, 128, 3, 8)         \
+    X(64, 4, 4, 1, 256, 4, 8) X(128, 16, 2, 1, 128, 3, 8) X(128, 8, 2, 1, 128, 4, 8)       \
+    X(128, 4, 4, 1, 128, 5, 8) X(256, 16, 4, 1, 64, 4, 8) X(256, 8, 4, 1, 128, 3, 8)       \
+    X(256, 4, 4, 1, 128, 4, 8)
 
 struct I8Args {
     const int8_t *x;
@@ -257,17 +256,45 @@ __global__ __launch_bounds__(NW * 64) void i8_pipe_kernel(I8Args a) {
     wait_loads<0>();  // no wave leaves LDS writes in flight
 }
 
-// y = bf16( (sum over the S slices) * (xs * ws) ), one output a thread.
+// y = bf16( (sum over the S slices) * (xs * ws) ), V outputs a thread (V = 4
+// where N allows it: one 16-byte load a slice, one 8-byte store).  Eight
+// slices' loads are issued before any is added.
+template <int V>
 __global__ __launch_bounds__(256) void i8_reduce(const int *part, const float *xs, const float *ws,
                                                  uint16_t *y, int N, int B, int S) {
-    const int n = blockIdx.x * 256 + threadIdx.x;
+    const int n = (blockIdx.x * 256 + threadIdx.x) * V;
     const int b = blockIdx.y;
     if (n >= N) return;
     const size_t slice = (size_t)B * N;
     const int *p = part + (size_t)b * N + n;
-    int acc = 0;
-    for (int s = 0; s < S; ++s) acc += p[s * slice];
-    y[(size_t)b * N + n] = round_bf16(scaled(acc, xs[b], ws[n]));
+    int acc[V] = {};
+    for (int s0 = 0; s0 < S; s0 += 8) {
+        int v[8][V];
+#pragma unroll
+        for (int s = 0; s < 8; ++s) {
+            if (s0 + s >= S) continue;  // uniform
+            if constexpr (V == 4)
+                *reinterpret_cast<i32x4 *>(v[s]) = __builtin_nontemporal_load(
+                    reinterpret_cast<const i32x4 *>(p + (s0 + s) * slice));
+            else
+                v[s][0] = p[(s0 + s) * slice];
+        }
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            if (s0 + s < S)
+#pragma unroll
+                for (int i = 0; i < V; ++i) acc[i] += v[s][i];
+    }
+    uint16_t *to = y + (size_t)b * N + n;
+    if constexpr (V == 4) {
+        const f32x4 w = *reinterpret_cast<const f32x4 *>(ws + n);
+        unsigned o[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[i] = round_bf16(scaled(acc[i], xs[b], w[i]));
+        *reinterpret_cast<u32x2 *>(to) = u32x2{o[0] | o[1] << 16, o[2] | o[3] << 16};
+    } else {
+        *to = round_bf16(scaled(acc[0], xs[b], ws[n]));
+    }
 }
 
 // ---------------------------------------------------------------- host side
@@ -308,32 +335,72 @@ int check_i8_tactic(int bin, const proj_tactic_t &t, size_t lds) {
     return i8_lds_bytes(t) <= lds ? PROJ_OK : PROJ_EINVAL;
 }
 
+// The rule follows what was measured at the shapes of a layer and of its
+// shards (us; the read of the weight alone takes 18.3 at 104 MB, 55 at 354 MB
+// and 7 at 13 MB on the same card), by r, the weight rows a compute unit has
+// of an even share:
+//   r >= 100 (49376 x 7168, r = 193): the widest weight tiles, K whole.
+//     B = 16: 58.2, 32: 60.6, 64: 59.5 (8-row-tile groups 72), 128: 80.2
+//     (91 staggered), 256: 143.9 (156 and more with other tiles).
+//   r >= 20 (14560 x 7168, r = 57; 7168 x 12288, r = 28): K split so that a
+//     row range fills a group.  14560: B = 16: 21.4 (32.9 with K whole and 32-row
+//     groups), 64: 23.9, 128: 34.8, 256: 56.1.  7168: 19.6, 23.6, 31.3, 45.0
+//     (69 at half the split).
+//   below (3640 and 1820 x 7168): 16-row groups whose waves split K, or 64-row
+//     groups and more slices.  1820: B = 1: 8.3, 32: 10.4, 128: 15.5 (22.5 with
+//     the tiles of large r); 3640: B = 16: 9.5 (12.9), 200: 25.4 (28.5).
+// Two workgroups of four waves a compute unit carry the narrow batches: 58.2
+// against 64.3 for one of eight at 49376 x 7168.  A row pitch that is a
+// multiple of 4 KB takes staggered chunks (7168 x 12288, B = 16: 19.6 against
+// 19.8); others measured the same or worse with them.
 proj_tactic_t i8_rule(int N, int K, int bin, int cus) {
     proj_tactic_t t{};
     t.kernel = PROJ_KERNEL_I8_PIPE;
-    t.nw = 8;
-    t.kw = 1;
-    t.waves = 2;
-    t.depth = 3;
-    t.wpc = 1;
-    t.stagger = 1;
+    const double r = std::max(1.0, (double)N / cus);
+    const bool wide = r >= 100, few = r < 20;
+    auto tile = [&](int bcap, int rows, int waves, int kw, int kc, int depth, int nw, int fill) {
+        t.bcap = bcap;
+        t.rows = rows;
+        t.waves = waves;
+        t.kw = kw;
+        t.kc = kc;
+        t.depth = depth;
+        t.nw = nw;
+        t.wpc = nw == 4 ? 2 : 1;
+        t.split = std::max(1, std::min(8, (int)(fill / r)));
+        while (t.split > 1 && K / t.split < 2 * kc) --t.split;
+    };
     if (bin <= 16) {
-        t.bcap = 16; t.rows = 2; t.waves = 1; t.kw = 4; t.kc = 512; t.depth = 4;
+        if (few)
+            tile(16, 1, 1, 8, 512, K <= 2048 ? 4 : 8, 8, 16);
+        else
+            tile(16, 4, 1, 1, 512, 2, 4, 128);
     } else if (bin <= 32) {
-        t.bcap = 32; t.rows = 4; t.kc = 256; t.depth = 4;
+        if (few)
+            tile(32, 4, 1, 2, 512, 3, 8, 64);
+        else
+            tile(32, 8, 2, 1, 256, 3, 8, 128);
     } else if (bin <= 64) {
-        t.bcap = 64; t.rows = 8; t.kc = 256;
+        if (wide)
+            tile(64, 16, 2, 1, 128, 3, 8, 64);
+        else
+            tile(64, 4, 4, 1, 256, 4, 8, 64);
     } else if (bin <= 128) {
-        t.bcap = 128; t.rows = 16; t.kc = 128;
+        if (wide)
+            tile(128, 16, 2, 1, 128, 3, 8, 64);
+        else if (few)
+            tile(128, 4, 4, 1, 128, 5, 8, 64);
+        else
+            tile(128, 8, 2, 1, 128, 4, 8, 128);
     } else {
-        t.bcap = 256; t.rows = 8; t.waves = 4; t.kc = 128;
+        if (wide)
+            tile(256, 16, 4, 1, 64, 4, 8, 64);
+        else if (few)
+            tile(256, 4, 4, 1, 128, 4, 8, 64);
+        else
+            tile(256, 8, 4, 1, 128, 3, 8, 128);
     }
-    const long group = 16L * t.rows;
-    const long per_cu = std::max(1L, (long)N / cus);
-    long S = std::max(1L, (group + per_cu / 2) / per_cu);
-    S = std::min(S, 8L);
-    while (S > 1 && K / S < 4 * t.kc) --S;
-    t.split = (int)S;
+    t.stagger = K % 4096 == 0;
     return t;
 }
 
@@ -539,8 +606,13 @@ int proj_i8_run(const proj_i8_plan_t *p, int B, const void *x, long ldx, const v
     const hipStream_t st = static_cast<hipStream_t>(stream);
     hipError_t e = launch_i8(a, t, p->cus, st);
     if (e == hipSuccess && S > 1) {
-        hipLaunchKernelGGL(i8_reduce, dim3((p->N + 255) / 256, B), dim3(256), 0, st, a.part, a.xs,
-                           a.ws, a.y, a.N, a.B, S);
+        // four outputs a thread where rows of N stay 16-byte aligned
+        if (p->N % 4 == 0 && is_aligned(w_scale, 16))
+            hipLaunchKernelGGL(i8_reduce<4>, dim3((p->N + 1023) / 1024, B), dim3(256), 0, st,
+                               a.part, a.xs, a.ws, a.y, a.N, a.B, S);
+        else
+            hipLaunchKernelGGL(i8_reduce<1>, dim3((p->N + 255) / 256, B), dim3(256), 0, st, a.part,
+                               a.xs, a.ws, a.y, a.N, a.B, S);
         e = hipGetLastError();
     }
     if (e != hipSuccess) {
