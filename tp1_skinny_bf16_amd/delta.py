@@ -11,69 +11,78 @@ from __future__ import annotations
 
 import ctypes
 
+import torch
+
 from ._binding import (PLAN_HOST_ONLY, DeltaIO, _check, _lib, _on_current_device, _same_device,
                        _stream_handle)
 
 HEAD = 128
+_BF16, _FP32 = torch.bfloat16, torch.float32
 
 
 def _heads(t, name):
-    import torch
-    if t.dtype != torch.bfloat16:
+    """(rows, heads, row stride) of BF16 [rows, heads, 128]."""
+    if t.dtype is not _BF16:
         raise TypeError(f"{name} must be bfloat16")
     if t.dim() != 3 or t.shape[2] != HEAD:
         raise ValueError(f"{name} must be [rows, heads, {HEAD}]")
     rows, h, _ = t.shape
-    if rows > 0 and (t.stride(2) != 1 or (h > 1 and t.stride(1) != HEAD)):
+    ld, lh, one = t.stride()
+    if rows > 0 and (one != 1 or (h > 1 and lh != HEAD)):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
-    return rows, h, t.stride(0) if rows > 1 else h * HEAD
+    return rows, h, ld if rows > 1 else h * HEAD
+
+
+def _flat(t, rows, h, name):
+    """Row stride of BF16 [rows, heads]."""
+    if t.shape != (rows, h):
+        raise ValueError(f"{name} must be [rows, heads]" +
+                         (" or [rows, heads, 128]" if name == "f" else ""))
+    ld, one = t.stride()
+    if rows > 0 and h > 1 and one != 1:
+        raise ValueError(f"{name} must have unit column stride")
+    return ld if rows > 1 else h
 
 
 def _operands(q, k, v, f, b, a_log, dt_bias, state, out, scale, l2norm):
     """Checks what both forms take; returns (io, out, rows, heads, qk_heads, slots)."""
-    import torch
     rows, Hk, ldq = _heads(q, "q")
     rk, hk, ldk = _heads(k, "k")
     rv, H, ldv = _heads(v, "v")
-    if (rk, hk) != (rows, Hk) or rv != rows or Hk < 1 or H % Hk:
+    if rk != rows or hk != Hk or rv != rows or Hk < 1 or H % Hk:
         raise ValueError("q and k must have one shape, and v the same rows and a multiple of "
                          "their heads")
-    if f.dtype != torch.bfloat16 or b.dtype != torch.bfloat16:
+    if f.dtype is not _BF16 or b.dtype is not _BF16:
         raise TypeError("f and b must be bfloat16")
     head_gate = f.dim() == 2
     if head_gate:
-        if tuple(f.shape) != (rows, H) or (rows > 0 and H > 1 and f.stride(1) != 1):
-            raise ValueError("f must be [rows, heads] or [rows, heads, 128]")
-        ldf, gates = f.stride(0) if rows > 1 else H, (H,)
+        ldf, gates = _flat(f, rows, H, "f"), (H,)
     else:
         rf, hf, ldf = _heads(f, "f")
-        if (rf, hf) != (rows, H):
+        if rf != rows or hf != H:
             raise ValueError("f must be [rows, heads] or [rows, heads, 128]")
         gates = (H, HEAD)
-    if tuple(b.shape) != (rows, H) or (rows > 0 and H > 1 and b.stride(1) != 1):
-        raise ValueError("b must be [rows, heads] with unit column stride")
-    if a_log.dtype != torch.float32 or dt_bias.dtype != torch.float32 or \
-            state.dtype != torch.float32:
+    ldb = _flat(b, rows, H, "b")
+    if a_log.dtype is not _FP32 or dt_bias.dtype is not _FP32 or state.dtype is not _FP32:
         raise TypeError("a_log, dt_bias and state must be float32")
-    if tuple(a_log.shape) != (H,) or tuple(dt_bias.shape) != gates or \
+    if a_log.shape != (H,) or dt_bias.shape != gates or \
             not (a_log.is_contiguous() and dt_bias.is_contiguous()):
         raise ValueError(f"a_log must be [{H}] and dt_bias {list(gates)}, contiguous")
-    if state.dim() != 4 or tuple(state.shape[1:]) != (H, HEAD, HEAD) or state.shape[0] < 1 or \
-            not state.is_contiguous():
+    pool = state.shape[0]
+    if state.shape != (pool, H, HEAD, HEAD) or pool < 1 or not state.is_contiguous():
         raise ValueError(f"state must be contiguous [slots, {H}, {HEAD}, {HEAD}]")
     if out is None:
-        out = torch.empty((rows, H, HEAD), dtype=torch.bfloat16, device=v.device)
+        out = v.new_empty((rows, H, HEAD))
         ldo = H * HEAD
     else:
         ro, ho, ldo = _heads(out, "out")
-        if (ro, ho) != (rows, H):
+        if ro != rows or ho != H:
             raise ValueError("out must have the shape of v")
     io = DeltaIO(q.data_ptr(), k.data_ptr(), v.data_ptr(), f.data_ptr(), b.data_ptr(), ldq, ldk,
-                 ldv, ldf, b.stride(0) if rows > 1 else H, a_log.data_ptr(), dt_bias.data_ptr(),
-                 state.data_ptr(), out.data_ptr(), ldo,
-                 HEAD ** -0.5 if scale is None else float(scale), int(bool(l2norm)),
-                 int(head_gate))
-    return io, out, rows, H, Hk, state.shape[0]
+                 ldv, ldf, ldb, a_log.data_ptr(), dt_bias.data_ptr(), state.data_ptr(),
+                 out.data_ptr(), ldo, HEAD ** -0.5 if scale is None else scale, bool(l2norm),
+                 head_gate)
+    return io, out, rows, H, Hk, pool
 
 
 def delta_step(q, k, v, f, b, a_log, dt_bias, state, slots, *, tokens: int = 1, scale=None,
@@ -88,10 +97,9 @@ def delta_step(q, k, v, f, b, a_log, dt_bias, state, slots, *, tokens: int = 1, 
     [slots, heads, 128, 128] as [key, value].  scale multiplies q (128^-0.5
     unless given).  Column views of a packed projection output will do.
     """
-    import torch
     io, out, rows, H, Hk, pool = _operands(q, k, v, f, b, a_log, dt_bias, state, out, scale,
                                            l2norm)
-    if slots.dtype != torch.int32:
+    if slots.dtype is not torch.int32:
         raise TypeError("slots must be int32")
     if tokens < 1 or slots.dim() != 1 or slots.shape[0] * tokens != rows or \
             not slots.is_contiguous():
@@ -126,7 +134,6 @@ class DeltaPlan:
         self.rows = int(_lib().proj_delta_plan_rows(h))
         self.device = None
         if not host_only:
-            import torch
             self.device = torch.cuda.current_device()
 
     def close(self):

@@ -5,7 +5,9 @@ from __future__ import annotations
 
 import ctypes
 
-from ._binding import PLAN_HOST_ONLY, Tactic, _check, _lib, _same_device, _stream_handle, _Tactic
+import torch
+
+from ._binding import PLAN_HOST_ONLY, Tactic, _check, _lib, _stream_handle, _Tactic
 
 
 class PlanI8:
@@ -23,7 +25,6 @@ class PlanI8:
         self.host_only = host_only
         self.device = None
         if not host_only:
-            import torch
             self.device = torch.cuda.current_device()
 
     def close(self):
@@ -62,34 +63,37 @@ class PlanI8:
     def run_ptr(self, B: int, x: int, ldx: int, x_scale: int, w: int, w_scale: int, y: int,
                 stream: int = 0) -> int:
         """Raw call: returns the status code instead of raising."""
-        return _lib().proj_i8_run(self._h, int(B), x, int(ldx), x_scale, w, w_scale, y, stream)
+        return _lib().proj_i8_run(self._h, B, x, ldx, x_scale, w, w_scale, y, stream)
 
     def run(self, x, x_scale, W, w_scale, out=None, *, stream=None):
         """out[B, N] = (x . W^T) * x_scale[:, None] * w_scale, BF16, of int8
         codes x [B, K] (rows may have a stride > K) and W [N, K]."""
-        import torch
-        if x.dtype != torch.int8 or W.dtype != torch.int8:
+        if x.dtype is not torch.int8 or W.dtype is not torch.int8:
             raise TypeError("x and W must be int8")
-        if x_scale.dtype != torch.float32 or w_scale.dtype != torch.float32:
+        if x_scale.dtype is not torch.float32 or w_scale.dtype is not torch.float32:
             raise TypeError("the scales must be float32")
-        if x.dim() != 2 or x.shape[1] != self.K or tuple(W.shape) != (self.N, self.K):
+        N, K = self.N, self.K
+        if x.dim() != 2 or x.shape[1] != K or W.shape != (N, K):
             raise ValueError(f"shapes x{tuple(x.shape)} W{tuple(W.shape)} do not "
-                             f"match the plan ({self.N} x {self.K})")
+                             f"match the plan ({N} x {K})")
         B = x.shape[0]
-        if (B > 0 and x.stride(1) != 1) or not W.is_contiguous():
+        ldx, one = x.stride()
+        if (one != 1 and B > 0) or not W.is_contiguous():
             raise ValueError("x needs unit column stride and W must be contiguous")
-        if tuple(x_scale.shape) != (B,) or tuple(w_scale.shape) != (self.N,) or \
+        if x_scale.shape != (B,) or w_scale.shape != (N,) or \
                 not (x_scale.is_contiguous() and w_scale.is_contiguous()):
             raise ValueError("the scales must be contiguous, one a row of x and of W")
         if out is None:
-            out = torch.empty((B, self.N), dtype=torch.bfloat16, device=x.device)
-        elif tuple(out.shape) != (B, self.N) or not out.is_contiguous() or \
-                out.dtype != torch.bfloat16:
+            out = x.new_empty((B, N), dtype=torch.bfloat16)
+        elif out.shape != (B, N) or not out.is_contiguous() or out.dtype is not torch.bfloat16:
             raise ValueError("out must be a contiguous bfloat16 [B, N] tensor")
-        _same_device(x, x_scale, W, w_scale, out)
-        if self.device is not None and x.device.index != self.device:
-            raise ValueError(f"operands on cuda:{x.device.index}, the plan on cuda:{self.device}")
-        rc = self.run_ptr(B, x.data_ptr(), x.stride(0) if B > 1 else self.K, x_scale.data_ptr(),
+        dev = x.get_device()
+        if dev < 0 or not (dev == W.get_device() == x_scale.get_device() ==
+                           w_scale.get_device() == out.get_device()):
+            raise ValueError("every operand must be a device tensor, all on one device")
+        if self.device is not None and dev != self.device:
+            raise ValueError(f"operands on cuda:{dev}, the plan on cuda:{self.device}")
+        rc = self.run_ptr(B, x.data_ptr(), ldx if B > 1 else K, x_scale.data_ptr(),
                           W.data_ptr(), w_scale.data_ptr(), out.data_ptr(),
                           _stream_handle(stream))
         if rc:
