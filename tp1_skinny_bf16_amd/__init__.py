@@ -18,6 +18,7 @@ from ._binding import (EXPORTS, KERNEL_IDS, KERNEL_NAMES,  # noqa: F401
 from ._binding import KERNEL_I8_PIPE  # noqa: F401
 from .delta import DeltaPlan, delta_step  # noqa: F401
 from .front import MoeFront  # noqa: F401
+from .kda import KdaLayer, KdaStack  # noqa: F401
 from .layers import LayerStack  # noqa: F401
 from .norm import quant_rows, rms_norm, rms_norm_i8  # noqa: F401
 from .proj_i8 import PlanI8  # noqa: F401
