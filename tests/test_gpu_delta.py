@@ -202,6 +202,33 @@ def test_a_prompt_in_pieces_continues_its_state():
     check("prompt in pieces", c, [(0, total, 0)], torch.cat(outs), d["state"], total)
 
 
+@pytest.mark.parametrize("lens,heads,gate", [([4000], 48, False), ([1500, 40, 1700, 900], 40, True),
+                                             ([130] * 40, 24, False)])
+def test_many_chunks_against_the_recurrent_form(lens, heads, gate):
+    # enough chunks and heads for several segments; the recurrent form holds
+    # everything in FP32 and is itself checked against 64 bits above
+    c = delta_inputs(sum(lens), heads, heads, gate, len(lens), seed=31)
+    seqs, out, d = run_plan(c, lens, list(range(len(lens))))
+    e = to_device(c)
+    q, k, v, b = columns(e)
+    want = torch.empty_like(out)
+    for r0, n, slot in seqs:
+        which = torch.tensor([slot], dtype=torch.int32, device=DEV)
+        for r in range(r0, r0 + n, 500):
+            at = slice(r, min(r + 500, r0 + n))
+            want[at] = tp.delta_step(q[at], k[at], v[at], e["f"][at], b[at], e["a_log"],
+                                     e["dt_bias"], e["state"], which, tokens=at.stop - r)
+    torch.cuda.synchronize()
+    rel = ((d["state"] - e["state"]).norm() / e["state"].norm()).item()
+    diff = (out.double() - want.double()).norm().item() / want.double().norm().item()
+    say(f"[{len(lens)} sequences, {sum(lens)} rows, H={heads}] states differ by {rel:.1e}, "
+        f"outputs by {diff:.1e}")
+    # both within 2^-20 of 64 bits; outputs differ where one rounds up and the
+    # other down: at most a BF16 step (2 U16), on a part of the values
+    assert rel <= 2.0 ** -19
+    assert diff <= U16
+
+
 def test_sequences_extreme_gates():
     # tokens that clear the state, keep it, or do so in some channels, at the
     # edges of chunks and in a row

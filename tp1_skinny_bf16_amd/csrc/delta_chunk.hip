@@ -668,9 +668,14 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 // loaded as soon as this one's are used); S and R meet in LDS as FP16 pairs.
 // Two barriers a chunk.
 //
-// The scales of S and R are common to the waves without another exchange:
-// |R| <= max |v| + sqrt(128) max |S| (|k e^G| <= 1), and the S of the next
-// chunk is at most max |S| + 64 max |R|; both maxima come with the operands.
+// The scales of S and R are common to the waves without an exchange: a token
+// adds at most |v| to the 2-norm of a column of S (|k| <= 1, beta <= 1, decays
+// <= 1), so a bound of the column norms grows by 64 max |v| a chunk, and |R|
+// <= max |v| + that bound.  The bound starts from the largest |S| and is
+// taken from it again every 16 chunks, where it is at most 2^10 max |v| too
+// large: FP16 pairs under a scale 2^13 too small still hold 2^-24 of the
+// largest value.  (A maximum over a wave costs 300 cycles, two a chunk were a
+// tenth of the scan.)
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ Scale scale_below(float bound) {
     return scale_for(__float_as_uint(fminf(bound, 3e38f)));
@@ -680,7 +685,59 @@ __device__ __forceinline__ float largest(u32x4 t) {
     return __uint_as_float(x > y ? x : y);
 }
 
+// A chunk's operands of one wave.
 template <int CT>
+struct ChunkOperands {
+    Split k[4], m[2][2];
+    u32x4 q[4], p[2], vtop;
+    u32x2 v[CT];
+    f32x4 d[2];
+
+    // what step s over channels of R takes
+    __device__ __forceinline__ void load_step(const char *at, int s, int w, int lane) {
+        const char *from = at + w * kWsWave + lane * 16;
+        k[s].hi = *reinterpret_cast<const u32x4 *>(from + ws_k(s));
+        k[s].lo = *reinterpret_cast<const u32x4 *>(from + ws_k(s) + 1024);
+        q[s] = *reinterpret_cast<const u32x4 *>(from + ws_q(s));
+    }
+    __device__ __forceinline__ void load_values(const char *at, int w, int lane, int part) {
+#pragma unroll
+        for (int i = 0; i < CT; ++i)
+            v[i] = *reinterpret_cast<const u32x2 *>(at + w * kWsWave + ws_v(0) +
+                                                    (part * CT + i) * 512 + lane * 8);
+        vtop = *reinterpret_cast<const u32x4 *>(at + kWsTop);
+    }
+    // what step st over tokens of S' takes
+    __device__ __forceinline__ void load_tokens(const char *at, int st, int w, int lane) {
+        const char *from = at + w * kWsWave + lane * 16;
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+            m[hf][st].hi = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st));
+            m[hf][st].lo = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st) + 1024);
+        }
+        if (st == 0 || w >= 2) p[st] = *reinterpret_cast<const u32x4 *>(from + ws_p(st));
+    }
+    __device__ __forceinline__ void load_decays(const char *at, int w, int lane) {
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf)
+            d[hf] = *reinterpret_cast<const f32x4 *>(
+                at + kWsD + (32 * w + 8 * (lane >> 4) + 4 * hf) * 4);
+    }
+    __device__ __forceinline__ void load(const char *at, int w, int lane, int part) {
+#pragma unroll
+        for (int s = 0; s < 4; ++s) load_step(at, s, w, lane);
+        load_values(at, w, lane, part);
+        load_tokens(at, 0, w, lane);
+        load_tokens(at, 1, w, lane);
+        load_decays(at, w, lane);
+    }
+};
+
+// AHEAD = 0: one set of operands, each half reloaded once it is used.  AHEAD
+// = 1 or 2: that many chunks loaded ahead, between the products (a scan that
+// has the compute unit to itself, where nothing else covers the latency): 21
+// chunks of 12 heads take 39 us, 58 with all loads at the chunk's start.
+template <int CT, int AHEAD>
 __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int rows, int slot,
                                              int h, int part, const char *ws, size_t ws_step,
                                              char *lds) {
@@ -691,52 +748,33 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
     unsigned *tops = reinterpret_cast<unsigned *>(lds + lds_tops(CT));
     float *state = a.state + ((size_t)slot * a.H + h) * (kHead * kHead) +
                    (size_t)(32 * w + 8 * lg) * kHead + part * (16 * CT) + lr;
+    const int chunks = (rows + kC - 1) / kC;
+    ChunkOperands<CT> ops[AHEAD + 1];
+    // a chunk's place, or the last one's past the end (read again, unused)
+    auto place = [&](int c) { return ws + (size_t)min(c, chunks - 1) * ws_step; };
     f32x4 S[2][CT];
-    unsigned top = 0;
+#pragma unroll
+    for (int i = 0; i < (AHEAD ? AHEAD : 1); ++i) {
+        ops[i].load(place(i), w, lane, part);
+    }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int v = 0; v < CT; ++v) {
+        for (int v = 0; v < CT; ++v)
 #pragma unroll
             for (int r = 0; r < 4; ++r) S[hf][v][r] = state[(4 * hf + r) * kHead + v * 16];
-            top = top_of(S[hf][v], top);
-        }
-    // a chunk's operands of this wave
-    Split kf[4], mf[2][2];
-    u32x4 qf[4], pf[2], vtop;
-    u32x2 vf[CT];
-    f32x4 df[2];
-    auto load_first = [&](const char *at) {  // what R takes
-        const char *from = at + w * kWsWave + lane * 16;
+    auto measure = [&]() {  // this wave's largest |S|, for the others
+        unsigned top = 0;
 #pragma unroll
-        for (int s = 0; s < 4; ++s) {
-            kf[s].hi = *reinterpret_cast<const u32x4 *>(from + ws_k(s));
-            kf[s].lo = *reinterpret_cast<const u32x4 *>(from + ws_k(s) + 1024);
-            qf[s] = *reinterpret_cast<const u32x4 *>(from + ws_q(s));
-        }
+        for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int v = 0; v < CT; ++v)
-            vf[v] = *reinterpret_cast<const u32x2 *>(at + w * kWsWave + ws_v(0) +
-                                                     (part * CT + v) * 512 + lane * 8);
-        vtop = *reinterpret_cast<const u32x4 *>(at + kWsTop);
+            for (int v = 0; v < CT; ++v) top = top_of(S[hf][v], top);
+        top = max64(top);
+        if (lane == 0) tops[w] = top;
     };
-    auto load_second = [&](const char *at) {  // what S takes
-        const char *from = at + w * kWsWave + lane * 16;
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-#pragma unroll
-            for (int st = 0; st < 2; ++st) {
-                mf[hf][st].hi = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st));
-                mf[hf][st].lo = *reinterpret_cast<const u32x4 *>(from + ws_m(hf, st) + 1024);
-            }
-            df[hf] = *reinterpret_cast<const f32x4 *>(at + kWsD + (32 * w + 8 * lg + 4 * hf) * 4);
-        }
-        pf[0] = *reinterpret_cast<const u32x4 *>(from + ws_p(0));
-        if (w >= 2) pf[1] = *reinterpret_cast<const u32x4 *>(from + ws_p(1));
+    auto measured = [&]() {  // a bound of the columns' norms from the largest |S| of all
+        return 12.f * largest(*reinterpret_cast<const u32x4 *>(tops));
     };
-    load_first(ws);
-    load_second(ws);
-
     auto share = [&](float up) {  // this wave's channels of S, as operands of step s = w
 #pragma unroll
         for (int v = 0; v < CT; ++v) {
@@ -746,18 +784,20 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
             *reinterpret_cast<u32x4 *>(to + 1024) = x.lo;
         }
     };
-    top = max64(top);
-    if (lane == 0) tops[w] = top;
+    measure();
     __syncthreads();
-    Scale ss = scale_below(largest(*reinterpret_cast<const u32x4 *>(tops)));
+    float bound = measured();
+    Scale ss = scale_below(bound);
     share(ss.up);
+    uint16_t *out = a.out + (size_t)(row0 + w * 16 + lr) * a.ldo + h * kHead + part * (16 * CT) +
+                    lg * 4;
 
-    for (int r0 = 0; r0 < rows; r0 += kC) {
-        const int n = min(kC, rows - r0);
-        const char *next = r0 + kC < rows ? ws + ws_step : ws;  // past the end: read again, unused
-        __syncthreads();  // S and its maxima are there
-        const float smax = largest(*reinterpret_cast<const u32x4 *>(tops));
-        const Scale sr = scale_below(largest(vtop) + 12.f * smax);
+    auto chunk = [&](int c, ChunkOperands<CT> &now, ChunkOperands<CT> &later) {
+        const char *ahead = place(c + (AHEAD ? AHEAD : 1));
+        __syncthreads();  // S is there
+        if ((c & 15) == 15) bound = measured();
+        const float vmax = largest(now.vtop);
+        const Scale sr = scale_below(vmax + bound);
         f32x4 x[CT], y[CT], o[CT];
 #pragma unroll
         for (int v = 0; v < CT; ++v) x[v] = y[v] = o[v] = none;
@@ -768,21 +808,22 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                 const char *at = lds + lds_s(CT, s, v) + lane * 16;
                 const u32x4 bh = *reinterpret_cast<const u32x4 *>(at);
                 const u32x4 bl = *reinterpret_cast<const u32x4 *>(at + 1024);
-                x[v] = mfma_h(kf[s].hi, bl, x[v]);
-                y[v] = mfma_h(kf[s].hi, bh, y[v]);
-                o[v] = mfma_h(bh, qf[s], o[v]);
-                x[v] = mfma_h(kf[s].lo, bh, x[v]);
+                x[v] = mfma_h(now.k[s].hi, bl, x[v]);
+                y[v] = mfma_h(now.k[s].hi, bh, y[v]);
+                o[v] = mfma_h(bh, now.q[s], o[v]);
+                x[v] = mfma_h(now.k[s].lo, bh, x[v]);
+                if (v == CT - 1) {
+                    if constexpr (AHEAD > 0) later.load_step(ahead, s, w, lane);
+                }
             }
         const float back = ss.down / kUnit;
-        top = 0;
 #pragma unroll
         for (int v = 0; v < CT; ++v) {
-            const float vv[4] = {bf16_lo(vf[v].x), bf16_hi(vf[v].x), bf16_lo(vf[v].y),
-                                 bf16_hi(vf[v].y)};
+            const float vv[4] = {bf16_lo(now.v[v].x), bf16_hi(now.v[v].x), bf16_lo(now.v[v].y),
+                                 bf16_hi(now.v[v].y)};
             f32x4 R;
 #pragma unroll
             for (int r = 0; r < 4; ++r) R[r] = __builtin_fmaf(x[v][r] + y[v][r], back, vv[r]);
-            top = top_of(R, top);
             R *= sr.up;
             const unsigned h0 = settled(pack_h(R[0], R[1])), h1 = settled(pack_h(R[2], R[3]));
             char *to = lds + lds_r(CT, 0, v) + (w >> 1) * (CT * 2048) + lane * 16 + (w & 1) * 8;
@@ -791,11 +832,16 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                 u32x2{pack_h(R[0] - h_lo(h0), R[1] - h_hi(h0)),
                       pack_h(R[2] - h_lo(h1), R[3] - h_hi(h1))};
         }
-        load_first(next);
-        top = max64(top);
-        if (lane == 0) tops[4 + w] = top;
-        __syncthreads();  // R and its maxima are there; S's operands are free
-        const float bound = smax + 64.f * largest(*reinterpret_cast<const u32x4 *>(tops + 4));
+        if constexpr (AHEAD == 0) {
+#pragma unroll
+            for (int s = 0; s < 4; ++s) now.load_step(ahead, s, w, lane);
+            now.load_values(ahead, w, lane, part);
+        } else {
+            later.load_values(ahead, w, lane, part);
+        }
+        bound += 64.f * vmax;
+        ss = scale_below(bound);
+        __syncthreads();  // R is there; S's operands are free
         f32x4 u[2][CT], z[2][CT], ou[CT];
 #pragma unroll
         for (int v = 0; v < CT; ++v) u[0][v] = u[1][v] = z[0][v] = z[1][v] = ou[v] = none;
@@ -808,34 +854,37 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                 const u32x4 bl = *reinterpret_cast<const u32x4 *>(at + 1024);
 #pragma unroll
                 for (int hf = 0; hf < 2; ++hf) {
-                    u[hf][v] = mfma_h(mf[hf][st].hi, bl, u[hf][v]);
-                    z[hf][v] = mfma_h(mf[hf][st].hi, bh, z[hf][v]);
+                    u[hf][v] = mfma_h(now.m[hf][st].hi, bl, u[hf][v]);
+                    z[hf][v] = mfma_h(now.m[hf][st].hi, bh, z[hf][v]);
                 }
-                if (st == 0 || w >= 2) ou[v] = mfma_h(bh, pf[st], ou[v]);
+                if (st == 0 || w >= 2) ou[v] = mfma_h(bh, now.p[st], ou[v]);
 #pragma unroll
-                for (int hf = 0; hf < 2; ++hf) u[hf][v] = mfma_h(mf[hf][st].lo, bh, u[hf][v]);
+                for (int hf = 0; hf < 2; ++hf) u[hf][v] = mfma_h(now.m[hf][st].lo, bh, u[hf][v]);
+                if (v == CT - 1) {
+                    if constexpr (AHEAD > 0) later.load_tokens(ahead, st, w, lane);
+                }
             }
         const float rb = sr.down / kUnit;
-        top = 0;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-            for (int v = 0; v < CT; ++v) {
+            for (int v = 0; v < CT; ++v)
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     S[hf][v][r] = __builtin_fmaf(u[hf][v][r] + z[hf][v][r], rb,
-                                                 S[hf][v][r] * df[hf][r]);
-                top = top_of(S[hf][v], top);
-            }
-        load_second(next);
-        const float os = back * a.scale, ob = rb * a.scale;
-        ss = scale_below(bound);
+                                                 S[hf][v][r] * now.d[hf][r]);
         share(ss.up);
-        top = max64(top);
-        if (lane == 0) tops[w] = top;
-        if (w * 16 + lr < n) {
-            uint16_t *to = a.out + (size_t)(row0 + r0 + w * 16 + lr) * a.ldo + h * kHead +
-                           part * (16 * CT) + lg * 4;
+        if constexpr (AHEAD == 0) {
+            now.load_tokens(ahead, 0, w, lane);
+            now.load_tokens(ahead, 1, w, lane);
+            now.load_decays(ahead, w, lane);
+        } else {
+            later.load_decays(ahead, w, lane);
+        }
+        if ((c & 15) == 14) measure();
+        const float os = back * a.scale, ob = rb * a.scale;
+        if (c * kC + w * 16 + lr < rows) {
+            uint16_t *to = out + (size_t)(c * kC) * a.ldo;
 #pragma unroll
             for (int v = 0; v < CT; ++v) {
                 float e[4];
@@ -845,7 +894,18 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
                     u32x2{pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3])};
             }
         }
-        ws = next;
+    };
+    if constexpr (AHEAD == 0) {
+        for (int c = 0; c < chunks; ++c) chunk(c, ops[0], ops[0]);
+    } else {
+        constexpr int N = AHEAD + 1;  // the sets in turn
+        for (int c = 0; c < chunks; c += N) {
+            chunk(c, ops[0], ops[N - 1]);
+            if (c + 1 < chunks) chunk(c + 1, ops[1], ops[0]);
+            if constexpr (N == 3) {
+                if (c + 2 < chunks) chunk(c + 2, ops[2], ops[1]);
+            }
+        }
     }
 #pragma unroll
     for (int hf = 0; hf < 2; ++hf)
@@ -867,7 +927,7 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaS
     if (i < scans) {
         const int h = i / PARTS % a.H;
         const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
-        scan_columns<CT>(a, e[0], e[1], e[2], h, i % PARTS,
+        scan_columns<CT, 0>(a, e[0], e[1], e[2], h, i % PARTS,
                          scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
                          (size_t)a.H * kDeltaItemBytes, lds);
         return;
@@ -876,6 +936,19 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaS
     const int h = i % a.H, c = i / a.H;
     const int *e = prep.chunk_table + 2 * c;
     prepare_item<HEAD_GATE>(a, e[0], e[1], h, prep.ws + (size_t)i * kDeltaItemBytes, lds);
+}
+
+// A scan alone: one workgroup a compute unit, with registers to load ahead.
+template <int CT>
+__global__ __launch_bounds__(256, 1) void delta_scan_kernel(DeltaArgs a, DeltaSegment scan) {
+    extern __shared__ __align__(16) char lds[];
+    constexpr int PARTS = 8 / CT;
+    const int i = blockIdx.x;
+    const int h = i / PARTS % a.H;
+    const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
+    scan_columns<CT, CT == 2 ? 2 : 1>(a, e[0], e[1], e[2], h, i % PARTS,
+                        scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                        (size_t)a.H * kDeltaItemBytes, lds);
 }
 
 template <int CT, bool HEAD_GATE>
@@ -894,6 +967,14 @@ hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
                                hipStream_t st) {
     // 32 columns a workgroup while those leave compute units idle, 64 above
     const bool narrow = (long)scan.seqs * a.H * 2 <= cus / 2;
+    if (prep.chunks == 0) {
+        const dim3 grid((unsigned)(scan.seqs * a.H * (narrow ? 4 : 2)));
+        if (narrow)
+            hipLaunchKernelGGL(delta_scan_kernel<2>, grid, dim3(256), kDeltaLds, st, a, scan);
+        else
+            hipLaunchKernelGGL(delta_scan_kernel<4>, grid, dim3(256), kDeltaLds, st, a, scan);
+        return hipGetLastError();
+    }
     if (narrow)
         return head_gate ? launch<2, true>(a, scan, prep, st) : launch<2, false>(a, scan, prep, st);
     return head_gate ? launch<4, true>(a, scan, prep, st) : launch<4, false>(a, scan, prep, st);
@@ -905,6 +986,8 @@ hipError_t allow_delta_lds() {
         if (e == hipSuccess)
             e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kDeltaLds);
     };
+    one(reinterpret_cast<const void *>(&delta_scan_kernel<2>));
+    one(reinterpret_cast<const void *>(&delta_scan_kernel<4>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, true>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, false>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<4, true>));
