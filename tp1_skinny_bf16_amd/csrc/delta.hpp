@@ -39,7 +39,7 @@ struct DeltaSeqs {
 // The chunked form.
 constexpr int kDeltaChunk = 64;             // tokens a chunk
 constexpr int kDeltaItemBytes = 107520;     // workspace of a chunk and head
-constexpr int kDeltaLds = 81920;            // LDS of a workgroup: two a compute unit
+constexpr int kDeltaLds = 77824;            // LDS of a workgroup: two a compute unit
 
 // A segment of the chunks: which to prepare, and which sequences to carry on.
 struct DeltaSegment {

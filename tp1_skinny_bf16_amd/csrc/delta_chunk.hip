@@ -33,7 +33,7 @@
 // tokens up to i}) (e^{whole blocks between}) (e^{sum of b's tokens after
 // j}).  Inside a block the second factor is e^{-(sum up to j)} instead,
 // which grows, so those products are FP32 ones (v_mfma_f32_16x16x4), and a
-// block whose tokens decay a channel by more than 2^-58 takes an exact path
+// block whose tokens decay a channel by more than 2^-112 takes an exact path
 // on the vector unit (a running sum from i down to j).
 //
 // Layout.  A wave of `prepare` owns one block of 16 tokens; lane l holds
@@ -97,8 +97,9 @@ __device__ __forceinline__ f32x4 mfma_h(u32x4 a, u32x4 b, f32x4 c) {
                                                   __builtin_bit_cast(f16x8_t, b), c, 0, 0, 0);
 }
 
-// A block is mild if no channel decays by more than 2^-kMild over it.
-constexpr float kMild = 58.f;
+// A block is mild if no channel decays by more than 2^-kMild over it: then
+// 2^10 / (that decay) is still far from FP32's largest value.
+constexpr float kMild = 112.f;
 
 // What unit-bounded values are multiplied by before they become FP16 pairs.
 constexpr float kUnit = 1024.f;
@@ -426,7 +427,7 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
         if (mild) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // e^{-(sum up to j)}; el is at least 2^-58 here
+                // e^{-(sum up to j)}; el is at least 2^-112 here
                 const float r = kf[e] * __builtin_amdgcn_rcpf(el[s][e]);
                 Ad = __builtin_amdgcn_mfma_f32_16x16x4f32(x[e], r, Ad, 0, 0, 0);
                 Pd = __builtin_amdgcn_mfma_f32_16x16x4f32(r, y[e], Pd, 0, 0, 0);
