@@ -167,7 +167,8 @@ def run_plan(c, lens, slots, **kw):
     ([1], 2, 1, False), ([2, 1], 1, 1, True), ([15], 2, 2, False), ([16], 2, 2, True),
     ([17], 3, 1, False), ([31, 0, 33], 2, 2, False), ([63], 2, 2, False), ([64], 2, 1, True),
     ([65], 2, 2, False), ([127, 128, 129], 2, 2, True), ([200, 3, 1, 64, 100], 4, 2, False),
-    ([500], 2, 2, False), ([191, 320], 1, 1, True),
+    ([500], 2, 2, False), ([191, 320], 1, 1, True), ([1, 260], 2, 2, False),
+    ([300, 16, 5], 2, 1, True),
 ])
 def test_sequences_match_64_bits(lens, heads, qk, gate):
     c = delta_inputs(sum(lens), heads, qk, gate, len(lens) + 1, seed=sum(lens) + heads)
@@ -242,6 +243,21 @@ def test_sequences_extreme_gates():
     c["row"][20, o], c["row"][21, o + 1] = inf, -inf
     seqs, out, d = run_plan(c, [n], [0])
     check("sequences extreme gates", c, seqs, out, d["state"], n)
+
+
+@pytest.mark.parametrize("head_gate", [False, True])
+@pytest.mark.parametrize("heavy,every,at", [(35.0, 16, 0), (70.0, 16, 0), (74.0, 16, 7),
+                                            (90.0, 16, 0), (90.0, 16, 9), (40.0, 5, 2),
+                                            (60.0, 1, 0), (8.0, 1, 0)])
+def test_sequences_of_heavy_finite_gates(heavy, every, at, head_gate):
+    # tokens that decay the state by e^-heavy among mild ones: the tokens after
+    # them still weigh against each other by ratios near 1
+    n = 200
+    c = delta_inputs(n, 2, 2, head_gate, 1, seed=27)
+    c["a_log"][:] = 0.0
+    c["f"][at::every] = heavy
+    seqs, out, d = run_plan(c, [n], [0])
+    check(f"heavy gates {heavy}/{every}", c, seqs, out, d["state"], n)
 
 
 def test_sequences_of_repeated_keys_without_decay():

@@ -66,8 +66,10 @@ int check_io(const proj_delta_io_t *io, int H, int Hk, long rows, int n_slots, D
     return PROJ_OK;
 }
 
-// A sequence of at most this many rows runs token by token: a chunk costs
-// about as much however few of its 64 tokens there are.
+// Sequences of at most this many rows run token by token, unless they are
+// few beside the others' chunks: a chunk costs about as much however few of
+// its 64 tokens there are (20 us for all in one launch), a launch of the
+// recurrent kernel beside the chunks' 5 us and more.
 constexpr int kShortRows = 16;
 
 // Chunks and heads a segment prepares at a time: enough workgroups to fill
@@ -92,8 +94,16 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
         r += lens[i];
         t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
     }
+    long shorts = 0, chunks = 0;
+    for (int i = 0; i < n; ++i) {
+        if (lens[i] > kShortRows)
+            chunks += (lens[i] + kDeltaChunk - 1) / kDeltaChunk;
+        else if (lens[i] > 0)
+            ++shorts;
+    }
+    const int shortest = shorts * 4 <= chunks ? 1 : kShortRows + 1;  // rows that make a chunk
     for (int i = 0; i < n; ++i)
-        if (lens[i] > 0 && lens[i] <= kShortRows) {
+        if (lens[i] > 0 && lens[i] < shortest) {
             t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
             ++t.shorts;
         }
@@ -130,7 +140,7 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
     };
     std::vector<int> left;                  // sequences with chunks still to place
     for (int i = 0; i < n; ++i)
-        if (lens[i] > kShortRows) left.push_back(i);
+        if (lens[i] >= shortest) left.push_back(i);
     for (int at = 0; !left.empty(); ++at) {
         size_t keep = 0;
         for (const int i : left) {

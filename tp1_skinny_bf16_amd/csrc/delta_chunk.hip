@@ -34,7 +34,9 @@
 // j}).  Inside a block the second factor is e^{-(sum up to j)} instead,
 // which grows, so those products are FP32 ones (v_mfma_f32_16x16x4), and a
 // block whose tokens decay a channel by more than 2^-112 takes an exact path
-// on the vector unit (a running sum from i down to j).
+// on the vector unit (a running sum from i down to j).  A sum of up to 112 is
+// off by 2^-18, and so is its factor, but only in a channel that a token of
+// this block all but clears; the 128 channels' errors are independent.
 //
 // Layout.  A wave of `prepare` owns one block of 16 tokens; lane l holds
 // token l % 16 and, for s = 0..3, channels 32 s + 8 (l / 16) + 0..7, which is
@@ -98,7 +100,9 @@ __device__ __forceinline__ f32x4 mfma_h(u32x4 a, u32x4 b, f32x4 c) {
 }
 
 // A block is mild if no channel decays by more than 2^-kMild over it: then
-// 2^10 / (that decay) is still far from FP32's largest value.
+// 2^10 / (that decay) is still below FP32's largest value by 2^6.  At 2^-58,
+// where ordinary gates (rates of 1 to 16) leave one block in three to the
+// exact path, 8192 tokens of 96 heads take 1235 us, at 2^-112 974 us.
 constexpr float kMild = 112.f;
 
 // What unit-bounded values are multiplied by before they become FP16 pairs.
@@ -562,12 +566,37 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
 #pragma unroll
             for (int i = 0; i < 16; ++i) blk[i * 20 + lr] = x[i];
     }
-    u32x4 vv[4];
+    // ---- V in operand order: transposed, its own BF16 values.  Wave 0 takes
+    // block 3 too: its A and P are the fewest, wave 3's the most.
+    if (w < 3) {
+#pragma unroll 1
+        for (int vb = w; vb < 4; vb += 3) {
+            const bool here = vb * 16 + lr < n;
+            const uint16_t *from = a.v + (long)(row0 + vb * 16 + lr) * a.ldv + h * kHead + 8 * lg;
+            u32x4 vv[4];
 #pragma unroll
-    for (int s = 0; s < 4; ++s)
-        vv[s] = live ? *reinterpret_cast<const u32x4 *>(a.v + row * a.ldv + h * kHead + 32 * s +
-                                                        8 * lg)
-                     : zero;
+            for (int s = 0; s < 4; ++s)
+                vv[s] = here ? *reinterpret_cast<const u32x4 *>(from + 32 * s) : zero;
+            unsigned top = 0;
+#pragma unroll
+            for (int s = 0; s < 4; ++s)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    u32x4 sel = zero;  // column r picks value 16 hf + r
+                    const int e = 16 * hf + lr - 8 * lg;
+                    if (e >= 0 && e < 8)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
+                    const f32x4 x = mfma_bf(vv[s], sel, none);
+                    top = top_of(x, top);
+                    *reinterpret_cast<u32x2 *>(ws + vb * kWsWave + ws_v(2 * s + hf) + lane * 8) =
+                        u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
+                }
+            top = max64(top);
+            if (lane == 0) reinterpret_cast<unsigned *>(ws + kWsTop)[vb] = top;
+        }
+    }
     __syncthreads();  // 2: N below the diagonal, the inverses, P and K e^{G_64 - G} are there
 
     // ---- column block w of T, a block at a time: T_ww is the block's inverse,
@@ -595,26 +624,6 @@ __device__ __forceinline__ void prepare_item(const DeltaArgs &a, int row0, int n
             if (c < 3) t = -times(c < 3 ? c + 1 : 3, c < 3 ? c + 1 : 3, X[c < 3 ? c + 1 : 3], none);
         }
     }
-    // ---- V in operand order: transposed, its own BF16 values
-    unsigned top = 0;
-#pragma unroll
-    for (int s = 0; s < 4; ++s)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-            u32x4 sel = zero;  // column r picks value 16 hf + r
-            const int e = 16 * hf + lr - 8 * lg;
-            if (e >= 0 && e < 8)
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    sel[i] = e >> 1 == i ? (e & 1 ? 0x3F800000u : 0x3F80u) : 0u;
-            const f32x4 x = mfma_bf(vv[s], sel, none);
-            top = top_of(x, top);
-            *reinterpret_cast<u32x2 *>(wsw + ws_v(2 * s + hf) + lane * 8) =
-                u32x2{pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3])};
-        }
-    top = max64(top);
-    if (lane == 0) reinterpret_cast<unsigned *>(ws + kWsTop)[w] = top;
-
     // ---- columns of block w of M (as M^T: tokens j = 4 lg + r, channel lr of a tile) and of P T
     const float bj = betas[w * 16 + lr] * kUnit;
     const Split t0 = split_h(T[0], T[1], bj), t1 = split_h(T[2], T[3], bj);
