@@ -209,3 +209,29 @@ def test_bindings_refuse_host_and_mistyped_tensors():
         plan.run(**{**t, "state": torch.zeros(4, 4, 128, 128)})
     with pytest.raises(ValueError):
         tp.DeltaPlan([2, 1], [0], heads=4, n_slots=3, host_only=True)
+
+
+def test_bindings_refuse_rows_that_overlap():
+    # expanded rows have stride 0, which the C calls read as contiguous
+    bf = torch.bfloat16
+    x = torch.zeros(1, 64, dtype=bf).expand(3, 64)
+    full, w = torch.zeros(3, 64, dtype=bf), torch.zeros(64, dtype=bf)
+    half = torch.zeros(256, dtype=bf).as_strided((3, 64), (32, 1))
+    for bad in (x, half):
+        for call in (lambda: tp.rms_norm(bad, w), lambda: tp.rms_norm_i8(bad, w),
+                     lambda: tp.quant_rows(bad), lambda: tp.rms_norm(full, w, residual=bad)):
+            with pytest.raises(ValueError, match="overlap"):
+                call()
+    p = tp.PlanI8(64, 64, [4], host_only=True)
+    c, s = torch.zeros(1, 64, dtype=torch.int8).expand(3, 64), torch.zeros(3)
+    with pytest.raises(ValueError, match="overlap"):
+        p.run(c, s, torch.zeros(64, 64, dtype=torch.int8), torch.zeros(64))
+    t = dict(q=torch.zeros(2, 2, 128, dtype=bf), k=torch.zeros(2, 2, 128, dtype=bf),
+             v=torch.zeros(2, 4, 128, dtype=bf), f=torch.zeros(2, 4, dtype=bf),
+             b=torch.zeros(2, 4, dtype=bf), a_log=torch.zeros(4), dt_bias=torch.zeros(4),
+             state=torch.zeros(3, 4, 128, 128), slots=torch.zeros(2, dtype=torch.int32))
+    for name in ("q", "k", "v", "f", "b"):
+        with pytest.raises(ValueError, match="overlap"):
+            tp.delta_step(**{**t, name: t[name][:1].expand(t[name].shape)})
+    with pytest.raises(ValueError, match="overlap"):
+        tp.delta_step(**t, out=torch.zeros(1, 4, 128, dtype=bf).expand(2, 4, 128))

@@ -30,6 +30,8 @@ def _heads(t, name):
     ld, lh, one = t.stride()
     if rows > 0 and (one != 1 or (h > 1 and lh != HEAD)):
         raise ValueError(f"the heads of a row of {name} must be contiguous")
+    if rows > 1 and ld < h * HEAD:
+        raise ValueError(f"the rows of {name} overlap")
     return rows, h, ld if rows > 1 else h * HEAD
 
 
@@ -41,6 +43,8 @@ def _flat(t, rows, h, name):
     ld, one = t.stride()
     if rows > 0 and h > 1 and one != 1:
         raise ValueError(f"{name} must have unit column stride")
+    if rows > 1 and ld < h:
+        raise ValueError(f"the rows of {name} overlap")
     return ld if rows > 1 else h
 
 

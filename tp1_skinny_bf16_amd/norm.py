@@ -25,6 +25,8 @@ def _rows(x):
     ldx, one = x.stride()
     if one != 1 and rows > 0:
         raise ValueError("x must have unit column stride")
+    if rows > 1 and ldx < D:
+        raise ValueError("the rows of x overlap")
     return rows, D, ldx if rows > 1 else D
 
 
@@ -51,6 +53,8 @@ def _norm(x, weight, residual, eps, out, codes, scale, stream):
             raise ValueError("residual must have the shape of x and unit column stride")
         if rows > 1:
             ldr = residual.stride(0)
+            if ldr < D:
+                raise ValueError("the rows of residual overlap")
         rp = residual.data_ptr()
         tensors.append(residual)
     yp = cp = sp = None

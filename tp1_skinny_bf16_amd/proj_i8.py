@@ -80,6 +80,8 @@ class PlanI8:
         ldx, one = x.stride()
         if (one != 1 and B > 0) or not W.is_contiguous():
             raise ValueError("x needs unit column stride and W must be contiguous")
+        if B > 1 and ldx < K:
+            raise ValueError("the rows of x overlap")
         if x_scale.shape != (B,) or w_scale.shape != (N,) or \
                 not (x_scale.is_contiguous() and w_scale.is_contiguous()):
             raise ValueError("the scales must be contiguous, one a row of x and of W")
