@@ -392,7 +392,7 @@ int proj_ring_probe(const void *x, const void *w, int K, int rows, int piece, in
  * y.  The codes of a row of zeros are 0 with scale 0; a row with an infinity
  * or a NaN gets codes 0 and scale NaN, so that products with it are NaN.
  * The sum of squares is held in FP32: a row whose sum passes 3.4e38 comes
- * out as zeros.
+ * out as zeros.  With eps = 0 a row of zeros is 0 / 0: NaN, codes 0.
  *   rows, D  : rows >= 0 (0 is a no-op); 8 <= D <= PROJ_MAX_ROW, D % 8 == 0
  *   x        : BF16 [rows, D], row stride ldx (0 = D; ldx % 8 == 0)
  *   residual : NULL, or [rows, D] BF16 (FP32 with residual_fp32 = 1), row
@@ -449,7 +449,8 @@ size_t proj_i8_plan_workspace_bytes(const proj_i8_plan_t *plan);
  *     S <- diag(a) S;  u = beta (v - S^T k);  S <- S + k u^T;  o = S^T q
  * with a = exp(-exp(a_log[h]) * softplus(f + dt_bias)), a channel of the key
  * each (or, with head_gate, one a head), beta = sigmoid(b), q and k divided
- * by sqrt(|.|^2 + 1e-6) where l2norm is set, and q multiplied by scale.
+ * by sqrt(|.|^2 + 1e-6) where l2norm is set (squares summed in FP32: a vector
+ * longer than 1.8e19 becomes zero), and q multiplied by scale.
  * The operands of both forms (rows are tokens; strides in elements, 0 =
  * contiguous; a row's heads are contiguous, so the columns of a packed
  * projection output can be passed in place):
@@ -497,7 +498,13 @@ int proj_delta_step(const proj_delta_io_t *io, int heads, int qk_heads, int requ
  *                 no two alike; the lengths sum to at most
  *                 PROJ_DELTA_MAX_ROWS
  *   flags       : 0 or PROJ_PLAN_HOST_ONLY
- * Rows of out past the last sequence are left as they were.  The plan owns
+ * Rows of out past the last sequence are left as they were.
+ * With l2norm the sequences run in chunks of 64 rows: the state comes out as
+ * from FP32 arithmetic, to 2^-20 of its largest values (among those a head's
+ * state has held in the last 16 chunks), and an infinity or a NaN in a row of
+ * q, k or v may reach every row of its chunk.  Without l2norm, where a key
+ * may be longer than 1 and the chunks' sums with it, they run row by row, as
+ * proj_delta_step does: right, but slow for long sequences.  The plan owns
  * its device workspace (one stream at a time, like proj_plan's), and making
  * one waits for the device.  Errors as proj_plan and proj_run.
  */

@@ -178,6 +178,14 @@ def test_sequences_match_64_bits(lens, heads, qk, gate):
     assert torch.equal(d["state"][0].cpu(), c["state"][0])
 
 
+def test_sequences_without_norm_run_row_by_row():
+    lens = [90, 0, 3]
+    c = delta_inputs(sum(lens), 4, 2, False, 4, seed=20)
+    c["row"] *= 0.05          # |k| well under 1
+    seqs, out, d = run_plan(c, lens, [2, 1, 3], scale=0.7, l2norm=False)
+    check("sequences raw", c, seqs, out, d["state"], 90, scale=0.7, l2norm=False)
+
+
 def test_sequences_leave_rows_behind_the_last_one():
     lens, extra = [70, 5], 9
     c = delta_inputs(sum(lens) + extra, 2, 2, False, 2, seed=21)

@@ -164,3 +164,18 @@ def test_refusals():
         tp.KdaStack([], [4], heads=2)
     with pytest.raises(ValueError):
         tp.KdaStack(stack.layers, [4], heads=3)
+
+
+def test_refusals_leave_the_residual_as_it_was():
+    stack = make(1, 2, 2, [8])
+    state = [torch.zeros(9, 2, HEAD, HEAD, device=DEV)]
+    slots = torch.arange(8, dtype=torch.int32, device=DEV)
+    for rows, how in ((9, {"slots": torch.arange(9, dtype=torch.int32, device=DEV)}),
+                      (8, {"slots": slots[:7]}), (8, {"slots": slots, "tokens": 2}),
+                      (8, {"plan": tp.DeltaPlan([7], [0], heads=2, n_slots=9)}), (8, {})):
+        x = torch.ones(rows, D, dtype=torch.bfloat16, device=DEV)
+        r = torch.ones(rows, D, device=DEV)
+        with pytest.raises((ValueError, tp.ProjError)):
+            stack.run(x, r, state, **how)
+        torch.cuda.synchronize()
+        assert bool((r == 1).all())

@@ -171,3 +171,14 @@ def test_row_offsets_past_32_bits():
     one, s1 = tp.quant_rows(last[None])
     assert torch.equal(codes[-1:], one) and torch.equal(scale[-1:], s1)
     assert not codes[:4].any() and not codes[-5:-1].any()
+
+
+def test_a_row_of_zeros_without_eps():
+    x = torch.ones(3, 256, dtype=torch.bfloat16, device=DEV)
+    x[1] = 0
+    w = torch.ones(256, dtype=torch.bfloat16, device=DEV)
+    out = torch.empty_like(x)
+    codes, scale = tp.rms_norm_i8(x, w, eps=0.0, out=out)
+    torch.cuda.synchronize()
+    assert bool(out[1].isnan().all()) and bool(scale[1].isnan()) and not codes[1].any()
+    assert bool((out[::2] == 1).all()) and bool((codes[::2] == 127).all())

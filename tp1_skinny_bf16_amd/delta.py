@@ -161,7 +161,9 @@ class DeltaPlan:
             out=None, stream=None):
         """The operands of delta_step, with the plan's rows (more rows may
         follow; theirs in out are left as they were, and out must then be
-        given).  Updates state in place and returns out."""
+        given).  Updates state in place and returns out.  Without l2norm
+        (keys of any length) the rows of a sequence run one by one, which is
+        slow for long ones."""
         if out is None and q.dim() == 3 and q.shape[0] != self.rows:
             raise ValueError(f"{q.shape[0]} rows, the plan has {self.rows}: give out")
         io, out, rows, H, Hk, pool = _operands(q, k, v, f, b, a_log, dt_bias, state, out, scale,

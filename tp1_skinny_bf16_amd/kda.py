@@ -21,7 +21,7 @@ import dataclasses
 
 import torch
 
-from ._binding import Plan
+from ._binding import PROJ_EBATCH, Plan, ProjError
 from .delta import HEAD, delta_step
 from .norm import quant_rows, rms_norm_i8
 from .proj_i8 import PlanI8
@@ -65,6 +65,7 @@ class KdaStack:
                     ly.w_f.shape != (self.heads * HEAD, self.rank) or \
                     ly.w_o.shape != (self.D, self.heads * HEAD):
                 raise ValueError(f"layer {i} does not have the shape of layer 0")
+        self.most = max(batches)
         self.in_plan = PlanI8(self.N_in, self.D, batches)
         self.f_plan = Plan(self.heads * HEAD, self.rank, batches)
         self.o_plan = PlanI8(self.D, self.heads * HEAD, batches)
@@ -115,8 +116,13 @@ class KdaStack:
             raise ValueError("give slots (a decode step) or plan (sequences)")
         if len(states) != len(self.layers):
             raise ValueError("one state pool a layer")
+        # before the first layer changes the residual
+        if x.shape[0] > self.most:
+            raise ProjError(PROJ_EBATCH, f"{x.shape[0]} rows, planned for {self.most}")
         if plan is not None and plan.rows != x.shape[0]:
             raise ValueError(f"{x.shape[0]} rows, the plan has {plan.rows}")
+        if slots is not None and slots.shape[0] * tokens != x.shape[0]:
+            raise ValueError(f"{x.shape[0]} rows, the slots have {slots.shape[0]} x {tokens}")
         buf = self.buffers(x.shape[0]) if buf is None else buf
         for i, state in enumerate(states):
             x = self.run_layer(i, x, residual, state, buf, slots=slots, tokens=tokens, plan=plan,
