@@ -47,6 +47,7 @@ struct DeltaSegment {
     const int *seq_table;    // {first row, rows, slot, first chunk} a sequence
     char *ws;
     int chunks, seqs;
+    int longest;             // most chunks of one sequence here
 };
 
 hipError_t launch_delta_steps(const DeltaArgs &a, const DeltaSeqs &s, bool head_gate, int cus,

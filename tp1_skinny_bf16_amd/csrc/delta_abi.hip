@@ -3,9 +3,11 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
 #include <mutex>
 #include <new>
+#include <utility>
 #include <vector>
 
 #include "../../include/tp1_proj.h"
@@ -72,9 +74,13 @@ int check_io(const proj_delta_io_t *io, int H, int Hk, long rows, int n_slots, D
 // recurrent kernel beside the chunks' 5 us and more.
 constexpr int kShortRows = 16;
 
-// Chunks and heads a segment prepares at a time: enough workgroups to fill
-// the device, and two workspaces that stay inside the memory-side cache.
-constexpr long kSegmentItems = 2048;
+// Chunks and heads a segment prepares at a time, by the heads at work on
+// average.  Many: the launches' ragged ends cost, so few and large segments
+// (8192 tokens of 96 heads: 902 us, 923 with 2048 and 970 with 1024; two
+// workspaces of 440 MB).  Few: the scan's chain takes longer than the
+// preparation, of which only the first segment's is not hidden (24 heads: 327
+// us, 344 with 2048, 388 with 4096; 40 heads: 478, 464 and 522).
+long segment_items(long busy) { return busy <= 32 ? 1024 : busy <= 64 ? 2048 : 4096; }
 
 struct Tables {
     std::vector<int> words;                 // every table, one after another
@@ -94,12 +100,15 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
         r += lens[i];
         t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
     }
-    long shorts = 0, chunks = 0;
+    long shorts = 0, chunks = 0, longest = 1;
     for (int i = 0; i < n; ++i) {
-        if (lens[i] > kShortRows)
-            chunks += (lens[i] + kDeltaChunk - 1) / kDeltaChunk;
-        else if (lens[i] > 0)
+        const long c = (lens[i] + (long)kDeltaChunk - 1) / kDeltaChunk;
+        if (lens[i] > kShortRows) {
+            chunks += c;
+            longest = std::max(longest, c);
+        } else if (lens[i] > 0) {
             ++shorts;
+        }
     }
     const int shortest = shorts * 4 <= chunks ? 1 : kShortRows + 1;  // rows that make a chunk
     for (int i = 0; i < n; ++i)
@@ -107,7 +116,13 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
             t.words.insert(t.words.end(), {(int)row[i], lens[i], slots[i]});
             ++t.shorts;
         }
-    const int per = (int)std::max(1L, kSegmentItems / H);
+    // segments of one size: a small last one would leave the scan before it
+    // without preparations to run beside
+    if (shortest == 1) chunks += shorts;
+    const double items = (double)chunks * H;
+    const long parts =
+        std::max(1L, std::lround(items / segment_items(chunks * H / longest)));
+    const int per = (int)std::max(1L, (chunks + parts - 1) / parts);
     struct Chunk {
         int seq, at;
     };
@@ -124,16 +139,25 @@ Tables cut(int H, int n, const int *lens, const int *slots) {
             t.words.push_back(std::min(kDeltaChunk, lens[c.seq] - c.at * kDeltaChunk));
         }
         t.seq_at.push_back(t.words.size());
+        std::vector<std::pair<int, int>> runs;  // chunks of one sequence: {first, how many}
         for (size_t i = 0; i < seg.size();) {
             size_t j = i;
             while (j < seg.size() && seg[j].seq == seg[i].seq) ++j;
-            const Chunk &a = seg[i], &b = seg[j - 1];
-            const int end = std::min(lens[a.seq], (b.at + 1) * kDeltaChunk);
-            t.words.insert(t.words.end(), {(int)(row[a.seq] + (long)a.at * kDeltaChunk),
-                                           end - a.at * kDeltaChunk, slots[a.seq], (int)i});
-            ++s.seqs;
+            runs.push_back({(int)i, (int)(j - i)});
             i = j;
         }
+        // the longest first: whatever has to wait for a compute unit is short
+        std::stable_sort(runs.begin(), runs.end(), [](const auto &x, const auto &y) {
+            return x.second > y.second;
+        });
+        for (const auto &[i, m] : runs) {
+            const Chunk &a = seg[i], &b = seg[i + m - 1];
+            const int end = std::min(lens[a.seq], (b.at + 1) * kDeltaChunk);
+            t.words.insert(t.words.end(), {(int)(row[a.seq] + (long)a.at * kDeltaChunk),
+                                           end - a.at * kDeltaChunk, slots[a.seq], i});
+        }
+        s.seqs = (int)runs.size();
+        s.longest = runs[0].second;
         t.most = std::max(t.most, s.chunks);
         t.segments.push_back(s);
         seg.clear();

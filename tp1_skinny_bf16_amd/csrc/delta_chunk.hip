@@ -13,7 +13,7 @@
 // chunks before, so the work is in two parts:
 //   prepare (one workgroup a chunk and head): K e^G, Q e^G, M = (K e^{G_64 -
 //     G})^T T, P T and e^{G_64}, and V in operand order, to a workspace;
-//   scan (workgroups of four waves, 64 or 32 columns of a head's state each):
+//   scan (workgroups of four waves, 16, 32 or 64 columns of a head's state each):
 //     chunk after chunk R = V - (K e^G) S, O = (Q e^G) S + (P T) R,
 //     S' = diag(e^{G_64}) S + M R.
 //
@@ -925,6 +925,18 @@ __device__ __forceinline__ void scan_columns(const DeltaArgs &a, int row0, int r
             for (int r = 0; r < 4; ++r) state[(4 * hf + r) * kHead + v * 16] = S[hf][v][r];
 }
 
+// Which head (of all sequences) and which of its columns a scan's workgroup
+// takes.  Workgroups go to the eight XCDs in turn, each with an L2 of its
+// own: the workgroups of a head, which load the same operands, are eight
+// apart, so that one L2 fetches them once.
+template <int PARTS>
+__device__ __forceinline__ void scan_place(int i, int all, int *head, int *part) {
+    const int g = i / (8 * PARTS), r = i % (8 * PARTS);
+    const int heads = min(8, all - 8 * g);  // of this group
+    *head = 8 * g + r % heads;
+    *part = r / heads;
+}
+
 // A launch holds the scan of one segment (its workgroups come first) and the
 // preparation of the next, which do not depend on each other.
 template <int CT, bool HEAD_GATE>
@@ -932,14 +944,16 @@ __global__ __launch_bounds__(256, 2) void delta_chunk_kernel(DeltaArgs a, DeltaS
                                                              DeltaSegment prep) {
     extern __shared__ __align__(16) char lds[];
     constexpr int PARTS = 8 / CT;  // workgroups a head in the scan
-    const int scans = scan.seqs * a.H * PARTS;
+    const int all = scan.seqs * a.H, scans = all * PARTS;
     int i = blockIdx.x;
     if (i < scans) {
-        const int h = i / PARTS % a.H;
-        const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
-        scan_columns<CT, 0>(a, e[0], e[1], e[2], h, i % PARTS,
-                         scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
-                         (size_t)a.H * kDeltaItemBytes, lds);
+        int head, part;
+        scan_place<PARTS>(i, all, &head, &part);
+        const int h = head % a.H;
+        const int *e = scan.seq_table + 4 * (head / a.H);
+        scan_columns<CT, 0>(a, e[0], e[1], e[2], h, part,
+                            scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                            (size_t)a.H * kDeltaItemBytes, lds);
         return;
     }
     i -= scans;
@@ -953,12 +967,13 @@ template <int CT>
 __global__ __launch_bounds__(256, 1) void delta_scan_kernel(DeltaArgs a, DeltaSegment scan) {
     extern __shared__ __align__(16) char lds[];
     constexpr int PARTS = 8 / CT;
-    const int i = blockIdx.x;
-    const int h = i / PARTS % a.H;
-    const int *e = scan.seq_table + 4 * (i / PARTS / a.H);
-    scan_columns<CT, CT == 2 ? 2 : 1>(a, e[0], e[1], e[2], h, i % PARTS,
-                        scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
-                        (size_t)a.H * kDeltaItemBytes, lds);
+    int head, part;
+    scan_place<PARTS>(blockIdx.x, scan.seqs * a.H, &head, &part);
+    const int h = head % a.H;
+    const int *e = scan.seq_table + 4 * (head / a.H);
+    scan_columns<CT, CT == 4 ? 1 : 2>(a, e[0], e[1], e[2], h, part,
+                                      scan.ws + ((size_t)e[3] * a.H + h) * kDeltaItemBytes,
+                                      (size_t)a.H * kDeltaItemBytes, lds);
 }
 
 template <int CT, bool HEAD_GATE>
@@ -975,17 +990,28 @@ hipError_t launch(const DeltaArgs &a, const DeltaSegment &scan, const DeltaSegme
 hipError_t launch_delta_chunks(const DeltaArgs &a, const DeltaSegment &scan,
                                const DeltaSegment &prep, bool head_gate, int cus,
                                hipStream_t st) {
-    // 32 columns a workgroup while those leave compute units idle, 64 above
-    const bool narrow = (long)scan.seqs * a.H * 2 <= cus / 2;
+    // Columns a workgroup: the fewer, the shorter a chunk takes (a head's
+    // chunks are one chain), but each workgroup of a head loads its 104 KB of
+    // operands.  By the heads at work on average (a short sequence is soon
+    // done): 8192 tokens of 12 heads take 222 us with 16 columns, 277 with
+    // 32, 413 with 64; of 24 heads 327, 358 and 492; of 40 heads 565, 464 and
+    // 561; of 96 heads 1222, 1023 and 902.
+    const long all = (long)scan.seqs * a.H;
+    const long busy = scan.longest ? (long)scan.chunks * a.H / scan.longest : 0;
+    const int ct = busy <= cus / 8 ? 1 : busy <= cus / 4 ? 2 : 4;
     if (prep.chunks == 0) {
-        const dim3 grid((unsigned)(scan.seqs * a.H * (narrow ? 4 : 2)));
-        if (narrow)
+        const dim3 grid((unsigned)(all * (8 / ct)));
+        if (ct == 1)
+            hipLaunchKernelGGL(delta_scan_kernel<1>, grid, dim3(256), kDeltaLds, st, a, scan);
+        else if (ct == 2)
             hipLaunchKernelGGL(delta_scan_kernel<2>, grid, dim3(256), kDeltaLds, st, a, scan);
         else
             hipLaunchKernelGGL(delta_scan_kernel<4>, grid, dim3(256), kDeltaLds, st, a, scan);
         return hipGetLastError();
     }
-    if (narrow)
+    if (ct == 1)
+        return head_gate ? launch<1, true>(a, scan, prep, st) : launch<1, false>(a, scan, prep, st);
+    if (ct == 2)
         return head_gate ? launch<2, true>(a, scan, prep, st) : launch<2, false>(a, scan, prep, st);
     return head_gate ? launch<4, true>(a, scan, prep, st) : launch<4, false>(a, scan, prep, st);
 }
@@ -996,8 +1022,11 @@ hipError_t allow_delta_lds() {
         if (e == hipSuccess)
             e = hipFuncSetAttribute(f, hipFuncAttributeMaxDynamicSharedMemorySize, kDeltaLds);
     };
+    one(reinterpret_cast<const void *>(&delta_scan_kernel<1>));
     one(reinterpret_cast<const void *>(&delta_scan_kernel<2>));
     one(reinterpret_cast<const void *>(&delta_scan_kernel<4>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, true>));
+    one(reinterpret_cast<const void *>(&delta_chunk_kernel<1, false>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, true>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<2, false>));
     one(reinterpret_cast<const void *>(&delta_chunk_kernel<4, true>));
