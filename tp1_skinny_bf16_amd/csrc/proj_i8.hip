@@ -347,8 +347,10 @@ int check_i8_tactic(int bin, const proj_tactic_t &t, size_t lds) {
 //     groups), 64: 23.9, 128: 34.8, 256: 56.1.  7168: 19.6, 23.6, 31.3, 45.0
 //     (69 at half the split).
 //   below (3640 and 1820 x 7168): 16-row groups whose waves split K, or 64-row
-//     groups and more slices.  1820: B = 1: 8.3, 32: 10.4, 128: 15.5 (22.5 with
-//     the tiles of large r); 3640: B = 16: 9.5 (12.9), 200: 25.4 (28.5).
+//     groups and more slices.  1820: B = 1: 8.6 (8.9 with two slices, whose sum is a
+//     second launch), 32: 9.8, 128: 15.5 (22.5 with the tiles of large r);
+//     3640: B = 16: 9.4 (12.7 with two slices), 200: 25.4 (28.5).  896 x 12288,
+//     B = 1: 9.1 with four slices, 11.6 with one.
 // Two workgroups of four waves a compute unit carry the narrow batches: 58.2
 // against 64.3 for one of eight at 49376 x 7168.  A row pitch that is a
 // multiple of 4 KB takes staggered chunks (7168 x 12288, B = 16: 19.6 against
@@ -372,7 +374,7 @@ proj_tactic_t i8_rule(int N, int K, int bin, int cus) {
     };
     if (bin <= 16) {
         if (few)
-            tile(16, 1, 1, 8, 512, K <= 2048 ? 4 : 8, 8, 16);
+            tile(16, 1, 1, 8, 512, K <= 2048 ? 4 : 8, 8, 14);
         else
             tile(16, 4, 1, 1, 512, 2, 4, 128);
     } else if (bin <= 32) {
