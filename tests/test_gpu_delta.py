@@ -212,9 +212,12 @@ def test_a_prompt_in_pieces_continues_its_state():
 
 
 @pytest.mark.parametrize("lens,heads,gate", [([4000], 48, False), ([1500, 40, 1700, 900], 40, True),
-                                             ([130] * 40, 24, False)])
+                                             ([130] * 40, 24, False), ([6500], 24, True),
+                                             ([4500, 20, 1400], 48, False),
+                                             ([2100, 2100, 300], 96, False)])
 def test_many_chunks_against_the_recurrent_form(lens, heads, gate):
-    # enough chunks and heads for several segments; the recurrent form holds
+    # many chunks and heads, the last three in several segments with 16, 32 and
+    # 64 columns a workgroup; the recurrent form holds
     # everything in FP32 and is itself checked against 64 bits above
     c = delta_inputs(sum(lens), heads, heads, gate, len(lens), seed=31)
     seqs, out, d = run_plan(c, lens, list(range(len(lens))))
