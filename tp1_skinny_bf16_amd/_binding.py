@@ -158,7 +158,7 @@ def _lib():
     lib.proj_read_probe.argtypes = [vp, ctypes.c_size_t, vp, ctypes.c_int, vp]
     lib.proj_read_probe.restype = ctypes.c_int
     cl, cf, ip = ctypes.c_long, ctypes.c_float, ctypes.POINTER(ctypes.c_int)
-    tac, io = ctypes.POINTER(_Tactic), ctypes.POINTER(DeltaIO)
+    tac = ctypes.POINTER(_Tactic)
     for name, args in (
             ("proj_rms_norm", [ci, ci, vp, cl, vp, cl, ci, vp, cf, vp, vp, vp, vp]),
             ("proj_quant_rows", [ci, ci, vp, cl, vp, vp, vp]),
@@ -166,9 +166,9 @@ def _lib():
             ("proj_i8_run", [vp, ci, vp, cl, vp, vp, vp, vp, vp]),
             ("proj_i8_plan_tactic", [vp, ci, tac, ip]),
             ("proj_i8_plan_set_tactic", [vp, ci, tac]),
-            ("proj_delta_step", [io, ci, ci, ci, ci, vp, ci, vp]),
+            ("proj_delta_step", [vp, ci, ci, ci, ci, vp, ci, vp]),
             ("proj_delta_plan", [ci, ci, ci, ip, ip, ci, ctypes.c_uint, ctypes.POINTER(vp)]),
-            ("proj_delta_run", [vp, io, vp])):
+            ("proj_delta_run", [vp, vp, vp])):
         fn = getattr(lib, name)
         fn.argtypes, fn.restype = args, ci
     for name, res in (("proj_i8_free", None), ("proj_delta_free", None),

@@ -19,9 +19,10 @@ def _rows(x):
     """(rows, D, row stride) of BF16 rows."""
     if x.dtype is not _BF16:
         raise TypeError("x must be bfloat16")
-    if x.dim() != 2:
+    shape = x.shape
+    if len(shape) != 2:
         raise ValueError("x must be [rows, D]")
-    rows, D = x.shape
+    rows, D = shape
     ldx, one = x.stride()
     if one != 1 and rows > 0:
         raise ValueError("x must have unit column stride")
